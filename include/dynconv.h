@@ -310,6 +310,147 @@ typedef enum {
  */
 DYNCONV_API int dynconv_trace_next(int kernel, hipEvent_t start, hipEvent_t stop);
 
+/*
+ * ---- What follows the convolution on the Q/K/V path -------------------
+ *
+ * The layer's placement on the query, key and value projections (Placement)
+ * leaves a row [B, T, (n_heads + 2 n_kv_heads) head_dim] of heads side by
+ * side.  The calls below take that row on: rotary positions on its query and
+ * key heads, causal attention with grouped heads over whole sequences
+ * (forward and backward), and the one-token step over a cache.  All of them
+ * follow the rules above (caller-owned buffers, host-side checks before
+ * anything is enqueued, kernels only, bitwise determinism).
+ *
+ * With i a query token, j a key token of the same sequence, j <= i, and
+ * query head e reading key/value head e / (n_heads / n_kv_heads):
+ *   s[i,j] = scale q[i].k[j]      lse[i] = log sum_j exp(s[i,j])
+ *   p[i,j] = exp(s[i,j] - lse[i]) o[i] = sum_j p[i,j] v[j]
+ *   dv[j] = sum_i p[i,j] do[i]    ds[i,j] = p[i,j] (do[i].v[j] - do[i].o[i])
+ *   dq[i] = scale sum_j ds[i,j] k[j]   dk[j] = scale sum_i ds[i,j] q[i]
+ * (dk and dv summed over the query heads of the group).  Products are formed
+ * on the matrix cores with fp32 sums; the softmax statistics, lse and delta =
+ * do.o are fp32; with bf16 tensors p and ds are rounded to bf16 where they
+ * enter a product, after their sum has been taken in fp32.
+ *
+ * A token of no sequence has no keys: its o and its gradients are zero and
+ * its lse is -infinity.  What lies in masked places is never part of a
+ * result, infinities and NaN included: a later token, another document or
+ * the padding cannot reach a row that does not see it.
+ */
+
+/* A strided view [B, T, heads, head_dim] of a tensor in the I/O dtype, the
+ * last axis contiguous.  Strides in elements, >= 0, of axes longer than 1
+ * whole 16-byte vectors; data 16-byte aligned.  Inputs may repeat (stride 0);
+ * outputs may not overlap themselves.  Several views may interleave in one
+ * buffer (the q, k, v parts of a row). */
+typedef struct {
+  void *data;
+  int64_t batch, row, head;
+} dynconv_view;
+
+/* Sizes of an attention call.  head_dim: whole 16-byte vectors (a multiple of
+ * 8 for bf16, of 4 for fp32), at most 128.  n_heads % n_kv_heads == 0.
+ * scale: the factor on q.k, 0 for 1 / sqrt(head_dim); it must be finite and
+ * not negative.  cu_seqlens / n_seqs: packed documents as in dynconv_problem
+ * (B must be 1); tokens from cu_seqlens[n_seqs] on, if there are any, belong
+ * to no document.  Limits: T and B below 2^31, B * n_heads * ceil(T / 64) below
+ * 2^31, a row stride of at most 16 MiB. */
+typedef struct {
+  int64_t B, T;
+  int32_t n_heads, n_kv_heads, head_dim;
+  int32_t dtype; /* dynconv_dtype */
+  float scale;
+  int32_t reserved;
+  const int32_t *cu_seqlens;
+  int64_t n_seqs;
+} dynconv_attn;
+
+/* Rotary positions.  Pair m of the first rot_dim elements of a head is turned
+ * by the angle position * freqs[m]:
+ *   (a, b) -> factor (a cos - b sin, b cos + a sin)
+ * pairs (2m, 2m+1) when interleaved, else (m, m + rot_dim/2); the rest of the
+ * head is left as it is.  inverse: by minus the angle, which is the backward
+ * of the rotation.  freqs: device array of rot_dim/2 doubles, radians per
+ * position, 8-byte aligned.  The angle is formed and reduced to a fraction of
+ * a turn in fp64, so a position of any size keeps fp32 accuracy. */
+typedef struct {
+  int32_t rot_dim; /* even, 2 .. head_dim */
+  int32_t interleaved;
+  int32_t inverse;
+  float factor;
+  const double *freqs;
+} dynconv_rotary;
+
+/*
+ * The frequencies of a rotary plan, on the host: out[m], m < rot_dim/2, from
+ * f = base^(-2m/rot_dim), stretched for contexts longer than the trained one.
+ *   trained_len == 0: out = f / stretch (every position scaled)
+ *   trained_len > 0 : by wavelength.  With n = trained_len f / 2 pi the turns
+ *     a pair makes over the trained length: pairs of fast_turns or more keep
+ *     f, pairs of slow_turns or fewer get f / stretch, in between linear in n.
+ * DYNCONV_E_SHAPE for an odd or non-positive rot_dim, base <= 0, stretch < 1, trained_len
+ * < 0 or (with trained_len) fast_turns <= slow_turns.
+ */
+DYNCONV_API int dynconv_rope_freqs(int rot_dim, double base, double stretch, double trained_len, double slow_turns,
+                                   double fast_turns, double *out);
+
+/*
+ * y = rotary(x) on a->n_heads heads (n_kv_heads and scale are not used).
+ * positions: device int32 [B, T], contiguous, or NULL for the token's index
+ * in its row, or in its document with cu_seqlens (the padding counts on from
+ * the last document's end).  y may be x's own view (in place); any other
+ * overlap is refused.  Here head_dim and the strides may be any; a view of whole
+ * 16-byte vectors with pairs that fill them takes the fast kernel.
+ */
+DYNCONV_API int dynconv_rope(const dynconv_attn *a, const dynconv_rotary *r, const dynconv_view *x,
+                             const int32_t *positions, const dynconv_view *y, hipStream_t stream);
+
+/*
+ * Causal attention over whole sequences.
+ *   q        [B,T,n_heads,head_dim], k, v [B,T,n_kv_heads,head_dim]
+ *   o        output [B,T,n_heads,head_dim]
+ *   lse      NULL, or fp32 [B, n_heads, T], contiguous, for dynconv_attn_bwd
+ * No workspace.
+ */
+DYNCONV_API int dynconv_attn_fwd(const dynconv_attn *a, const dynconv_view *q, const dynconv_view *k,
+                                 const dynconv_view *v, const dynconv_view *o, float *lse, hipStream_t stream);
+
+/*
+ * Its backward: dq, dk, dv (overwritten) from the forward's inputs and
+ * outputs and d_o, the gradient of o.  workspace: 16-byte aligned, at least
+ * dynconv_attn_bwd_workspace_bytes(a).
+ */
+DYNCONV_API size_t dynconv_attn_bwd_workspace_bytes(const dynconv_attn *a);
+DYNCONV_API int dynconv_attn_bwd(const dynconv_attn *a, const dynconv_view *q, const dynconv_view *k,
+                                 const dynconv_view *v, const dynconv_view *o, const float *lse,
+                                 const dynconv_view *d_o, const dynconv_view *dq, const dynconv_view *dk,
+                                 const dynconv_view *dv, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+
+/*
+ * One token for each of B sequences (a->T must be 1, cu_seqlens NULL), the
+ * step that follows dynconv_decode.  lengths[b] (device int32) tokens of
+ * sequence b are in the cache; the new one has position lengths[b]:
+ *   q, k are turned by the rotary plan r (NULL: not turned), k and v stored in
+ *   cache row lengths[b], and o = attention of q over cache rows 0 .. lengths[b].
+ *   q, o             [B, 1, n_heads, head_dim]; k, v [B, 1, n_kv_heads, head_dim]
+ *   k_cache, v_cache [B, capacity, n_kv_heads, head_dim]; read and updated in
+ *                    place (one row), their other rows from lengths[b] on are not read
+ * A slot with lengths[b] < 0 or >= capacity is idle: its o is zero and its
+ * cache is not touched.  lengths is not advanced (the caller's, once all
+ * layers have run).  k is rounded to the I/O dtype as it is stored; q is not.
+ * r->inverse must be 0.
+ * workspace: 16-byte aligned, at least
+ * dynconv_attn_decode_workspace_bytes(a, capacity); it may be 0 bytes.
+ * B at most 65535.
+ */
+DYNCONV_API size_t dynconv_attn_decode_workspace_bytes(const dynconv_attn *a, int64_t capacity);
+DYNCONV_API int dynconv_attn_decode(const dynconv_attn *a, const dynconv_rotary *r, const dynconv_view *q,
+                                    const dynconv_view *k, const dynconv_view *v, const dynconv_view *k_cache,
+                                    const dynconv_view *v_cache, int64_t capacity, const int32_t *lengths,
+                                    const dynconv_view *o, void *workspace, size_t workspace_bytes,
+                                    hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -53,9 +53,27 @@ class GenGrad(ctypes.Structure):
                 ("dw0", ctypes.c_void_p)]
 
 
+class View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class Attn(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("n_heads", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int64)]
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("freqs", ctypes.c_void_p)]
+
+
 # names the C header declares; the CPU tests check each is exported
 EXPORTS = ("dynconv_fwd", "dynconv_fwd_proj", "dynconv_fwd_noalloc", "dynconv_bwd", "dynconv_decode", "dynconv_workspace_bytes",
-           "dynconv_gen_cache_bytes", "dynconv_status_str", "dynconv_abi_version", "dynconv_trace_next")
+           "dynconv_gen_cache_bytes", "dynconv_status_str", "dynconv_abi_version", "dynconv_trace_next",
+           "dynconv_rope_freqs", "dynconv_rope", "dynconv_attn_fwd", "dynconv_attn_bwd_workspace_bytes",
+           "dynconv_attn_bwd", "dynconv_attn_decode_workspace_bytes", "dynconv_attn_decode")
 DYNCONV_E_SCRATCH = -10
 NOALLOC_SCRATCH_BYTES = 16 << 20  # the static scratch of dynconv_fwd_noalloc
 
@@ -94,6 +112,17 @@ def lib() -> ctypes.CDLL:
         L.dynconv_abi_version.restype = ctypes.c_int
         L.dynconv_trace_next.argtypes = [ctypes.c_int, P, P]
         L.dynconv_trace_next.restype = ctypes.c_int
+        PA, PR, PV = ctypes.POINTER(Attn), ctypes.POINTER(Rotary), ctypes.POINTER(View)
+        D, SZ, I64 = ctypes.c_double, ctypes.c_size_t, ctypes.c_int64
+        L.dynconv_rope_freqs.argtypes = [ctypes.c_int, D, D, D, D, D, P]
+        L.dynconv_rope.argtypes = [PA, PR, PV, P, PV, P]
+        L.dynconv_attn_fwd.argtypes = [PA, PV, PV, PV, PV, P, P]
+        L.dynconv_attn_bwd_workspace_bytes.argtypes = [PA]
+        L.dynconv_attn_bwd_workspace_bytes.restype = SZ
+        L.dynconv_attn_bwd.argtypes = [PA, PV, PV, PV, PV, P, PV, PV, PV, PV, P, SZ, P]
+        L.dynconv_attn_decode_workspace_bytes.argtypes = [PA, I64]
+        L.dynconv_attn_decode_workspace_bytes.restype = SZ
+        L.dynconv_attn_decode.argtypes = [PA, PR, PV, PV, PV, PV, PV, I64, P, PV, P, SZ, P]
         _lib = L
     return _lib
 
@@ -314,3 +343,157 @@ class DynConvFn(torch.autograd.Function):
         cast = lambda t, ref: None if t is None or ref is None else t.to(ref.dtype)
         return (g.get("dh"), g["dx"], cast(g.get("dW"), W), cast(g.get("dA"), A),
                 cast(g.get("dU"), U), cast(g.get("dw0"), w0), None, None, None)
+
+
+# --- the Q/K/V path behind the convolution ------------------------------------------------------
+
+
+def _view(t: torch.Tensor, what: str, heads: int | None = None, like=None, dtype=None) -> View:
+    """View struct of a [B, T, heads, head_dim] tensor whose last axis is contiguous."""
+    if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+        raise ValueError(f"{what}: expected [B, T, heads, head_dim] with a contiguous last axis, got "
+                         f"{tuple(t.shape)} strides {t.stride()}")
+    if like is not None and (t.shape[0], t.shape[1], t.shape[3]) != like:
+        raise ValueError(f"{what}: sizes {tuple(t.shape)} do not fit [B, T, head_dim] = {like}")
+    if heads is not None and t.shape[2] != heads:
+        raise ValueError(f"{what}: {t.shape[2]} heads where {heads} were expected")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: {t.dtype} where {dtype} was expected")
+    if not t.is_cuda:
+        raise TypeError(f"{what} must be on the GPU")
+    s = t.stride()
+    return View(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _int32(t, what: str, shape: tuple | None = None):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+        raise TypeError(f"{what} must be a contiguous int32 tensor" + (f" of shape {shape}" if shape else ""))
+    if not t.is_cuda:
+        raise TypeError(f"{what} must be on the GPU")
+    return t.data_ptr()
+
+
+def _attn(q: torch.Tensor, n_kv_heads: int, scale, cu_seqlens) -> Attn:
+    B, T, H, hd = q.shape
+    if cu_seqlens is None:
+        return Attn(B, T, H, n_kv_heads, hd, _dtype_code(q.dtype), scale or 0.0, 0, None, 0)
+    if cu_seqlens.dim() != 1:
+        raise TypeError("cu_seqlens must be a contiguous 1-d int32 tensor")
+    return Attn(B, T, H, n_kv_heads, hd, _dtype_code(q.dtype), scale or 0.0, 0, _int32(cu_seqlens, "cu_seqlens"),
+                cu_seqlens.numel() - 1)
+
+
+def _rotary(freqs: torch.Tensor, interleaved: bool, inverse: bool, factor: float) -> Rotary:
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise TypeError("freqs must be a contiguous 1-d float64 tensor (radians per position, one per pair)")
+    if not freqs.is_cuda:
+        raise TypeError("freqs must be on the GPU")
+    return Rotary(2 * freqs.numel(), int(interleaved), int(inverse), factor, freqs.data_ptr())
+
+
+def dynconv_rope_freqs(rot_dim: int, base: float = 10000.0, *, stretch: float = 1.0, trained_len: float = 0.0,
+                       slow_turns: float = 1.0, fast_turns: float = 32.0, device="cuda") -> torch.Tensor:
+    """The frequencies of a rotary plan, float64 [rot_dim/2] on ``device``.
+
+    ``base ** (-2m / rot_dim)``; with ``stretch`` > 1 divided by it, for all
+    pairs, or with ``trained_len`` > 0 by wavelength: pairs that make
+    ``fast_turns`` or more turns over the trained length keep their frequency,
+    those of ``slow_turns`` or fewer are divided, linear in between."""
+    out = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float64)
+    _check(lib().dynconv_rope_freqs(int(rot_dim), base, stretch, trained_len, slow_turns, fast_turns,
+                                    out.data_ptr() or None), "dynconv_rope_freqs")
+    return out.to(device)
+
+
+def dynconv_rope(x, freqs, *, positions=None, cu_seqlens=None, interleaved=False, factor=1.0, inverse=False, out=None,
+                 stream=None):
+    """Rotary positions: x [B, T, heads, head_dim] (any strides) with its first
+    2 * len(freqs) elements turned, as a new tensor or into ``out`` (x itself:
+    in place).  positions: int32 [B, T], or the token's index in its row or,
+    with cu_seqlens, in its document.  inverse: the backward."""
+    a = _attn(x, 1, None, cu_seqlens)
+    r = _rotary(freqs, interleaved, inverse, factor)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    vx = _view(x, "x")
+    vy = _view(out, "out", x.shape[2], (x.shape[0], x.shape[1], x.shape[3]), x.dtype)
+    rc = lib().dynconv_rope(a, r, vx, _int32(positions, "positions", tuple(x.shape[:2])), vy, _stream(stream))
+    _check(rc, "dynconv_rope")
+    return out
+
+
+def dynconv_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, o=None, lse=None, want_lse=False, stream=None):
+    """Causal attention over whole sequences: q [B, T, n_heads, head_dim], k and
+    v [B, T, n_kv_heads, head_dim] (any strides with a contiguous last axis).
+    Returns o (and lse, fp32 [B, n_heads, T], when want_lse).  scale: default
+    1 / sqrt(head_dim).  cu_seqlens: packed documents (B must be 1)."""
+    G, dt = k.shape[2], q.dtype
+    a = _attn(q, G, scale, cu_seqlens)
+    like = (a.B, a.T, a.head_dim)
+    if o is None:
+        o = torch.empty(q.shape, dtype=dt, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((a.B, a.n_heads, a.T), dtype=torch.float32, device=q.device)
+    rc = lib().dynconv_attn_fwd(a, _view(q, "q"), _view(k, "k", G, like, dt), _view(v, "v", G, like, dt),
+                                _view(o, "o", a.n_heads, like, dt), _lse(lse, a), _stream(stream))
+    _check(rc, "dynconv_attn_fwd")
+    return (o, lse) if want_lse else o
+
+
+def _lse(lse, a: Attn):
+    if lse is None:
+        return None
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (a.B, a.n_heads, a.T) or not lse.is_contiguous():
+        raise TypeError(f"lse must be a contiguous float32 tensor [{a.B}, {a.n_heads}, {a.T}]")
+    if not lse.is_cuda:
+        raise TypeError("lse must be on the GPU")
+    return lse.data_ptr()
+
+
+def dynconv_attn_bwd(q, k, v, o, lse, d_o, *, scale=None, cu_seqlens=None, out=None, workspace=None, stream=None):
+    """Backward of dynconv_attn_fwd from its inputs, o, lse and d_o.  Returns
+    dict(dq, dk, dv); ``out`` may hold any of them (views of one gradient row,
+    for instance)."""
+    G, dt = k.shape[2], q.dtype
+    a = _attn(q, G, scale, cu_seqlens)
+    like, H = (a.B, a.T, a.head_dim), a.n_heads
+    g = dict(out or {})
+    for name, t in (("dq", q), ("dk", k), ("dv", v)):
+        if name not in g:
+            g[name] = torch.empty(t.shape, dtype=dt, device=q.device)
+    ws = _workspace(int(lib().dynconv_attn_bwd_workspace_bytes(a)), q.device, workspace)
+    rc = lib().dynconv_attn_bwd(
+        a, _view(q, "q"), _view(k, "k", G, like, dt), _view(v, "v", G, like, dt), _view(o, "o", H, like, dt),
+        _lse(lse, a), _view(d_o, "d_o", H, like, dt), _view(g["dq"], "dq", H, like, dt),
+        _view(g["dk"], "dk", G, like, dt), _view(g["dv"], "dv", G, like, dt), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream))
+    _check(rc, "dynconv_attn_bwd")
+    return g
+
+
+def dynconv_attn_decode(q, k, v, k_cache, v_cache, lengths, *, scale=None, freqs=None, interleaved=False, factor=1.0,
+                        o=None, workspace=None, stream=None):
+    """One token per sequence: q [B, n_heads, head_dim], k and v [B, n_kv_heads,
+    head_dim], caches [B, capacity, n_kv_heads, head_dim], lengths int32 [B] (the
+    tokens in each cache; the new one's position).  q and k are turned by the
+    rotary plan (freqs None: not), k and v stored in the caches' rows lengths[b],
+    and o [B, n_heads, head_dim] returned.  A slot with lengths[b] < 0 (or a full
+    one) is idle: its o is zero."""
+    q4, k4, v4 = q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1)
+    G, dt, cap = k.shape[1], q.dtype, k_cache.shape[1]
+    a = _attn(q4, G, scale, None)
+    like, rows = (a.B, 1, a.head_dim), (a.B, cap, a.head_dim)
+    if o is None:
+        o = torch.empty(q.shape, dtype=dt, device=q.device)
+    r = None if freqs is None else _rotary(freqs, interleaved, False, factor)
+    nbytes = int(lib().dynconv_attn_decode_workspace_bytes(a, cap))
+    ws = _workspace(nbytes, q.device, workspace) if nbytes else None
+    rc = lib().dynconv_attn_decode(
+        a, r, _view(q4, "q"), _view(k4, "k", G, like, dt), _view(v4, "v", G, like, dt),
+        _view(k_cache, "k_cache", G, rows, dt), _view(v_cache, "v_cache", G, rows, dt), cap,
+        _int32(lengths, "lengths", (a.B,)), _view(o.unsqueeze(1), "o", a.n_heads, like, dt), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _check(rc, "dynconv_attn_decode")
+    return o

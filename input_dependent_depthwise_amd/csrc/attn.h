@@ -1,0 +1,339 @@
+// attn.h -- internal pieces of libdynconv's attention kernels: arguments,
+// document bounds, LDS tiles and matrix-core fragments (attn_fwd.hip,
+// attn_bwd.hip).
+//
+// All three attention kernels have the same form.  A wave owns 32 rows (the
+// queries in the forward and in dq, the keys in dk/dv), one per lane column;
+// the rows of the other side stream through LDS in tiles.  Scores are formed
+// with the streamed rows as the A operand, so D[streamed row][owned row] puts
+// one owned row in each lane pair (l, l + 32): softmax statistics are lane
+// scalars, and a second product that sums over the streamed rows takes its B
+// operand from the very registers that hold the scores, because the order of
+// a product's summed index is free as long as the A operand (read from LDS
+// by columns) follows it.
+#pragma once
+
+#include "bufio.h"
+#include "mfma.h"
+
+namespace dynconv {
+
+struct AttnView {  // strides in bytes
+  char *p;
+  int64_t batch, row, head;
+};
+
+struct AttnArgs {
+  AttnView q, k, v, o;
+  AttnView d_o, dq, dk, dv;  // backward
+  float *lse;                // [B, H, T]
+  float *delta;              // backward workspace: do . o, [B, H, T]
+  float *part;               // backward workspace: dk / dv of the splits of a group (n_split > 1)
+  int B, T, H, G, hd;
+  int n_split;  // dk/dv: blocks that share a key/value head's query heads
+  float scale;
+  const int32_t *cu;
+  int n_seqs;
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 16 bytes of T as fp32 values (8 bf16 or 4 floats).
+template <typename T>
+__device__ __forceinline__ void widen(const uint4 &r, float (&f)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      f[i] = __uint_as_float(w[i]);
+    } else {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+// Tokens of the row that belong to a document (all T without packing).
+__device__ __forceinline__ int tokens_in_docs(const int32_t *cu, int n_seqs, int T) {
+  if (!cu) return T;
+  return min(max(cu[n_seqs], 0), T);
+}
+
+// The document of token t: [start, end).  A token of none gets start > t and
+// end = 0.  Whatever the offsets hold, start >= 0 and end <= T.
+__device__ __forceinline__ void doc_of(const int32_t *cu, int n_seqs, int T, int t, int &start, int &end) {
+  if (!cu) {
+    start = t < T ? 0 : T;
+    end = t < T ? T : 0;
+    return;
+  }
+  int lo = 0, hi = n_seqs;  // the first j in [1, n_seqs] with cu[j] > t, else n_seqs + 1
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid + 1] > t) hi = mid;
+    else lo = mid + 1;
+  }
+  if (lo >= n_seqs || t >= T) {
+    start = T;
+    end = 0;
+    return;
+  }
+  start = min(max(cu[lo], 0), t);
+  end = min(cu[lo + 1], T);
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The other half wave's value (lane l ^ 32).
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// D[32x32] += A B over one step of the summed index: 16 (bf16) or 8 (fp32)
+// values, of which a lane of half h = l / 32 holds one 16-byte chunk.
+template <typename T>
+__device__ __forceinline__ void mma_step(const uint4 &a, const uint4 &b, f32x16 &c) {
+  if constexpr (sizeof(T) == 2) {
+    c = mfma32(as_bf16x8(a), as_bf16x8(b), c);
+  } else {
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+  }
+}
+
+// A tile of rows of DH elements in LDS, row-major, the 16-byte chunks of a row
+// permuted by an XOR that depends on the row: chunk j of row r lies at j ^
+// f(r).  f takes 16 consecutive rows to different banks for reads by rows (16
+// lanes, one chunk each), and 4 consecutive rows to different 64-byte groups
+// for the transposing reads (4 rows x 64 bytes for a half wave).
+template <typename T, int DH>
+struct Tile {
+  static constexpr int E = 16 / (int)sizeof(T);  // elements of a chunk
+  static constexpr int NC = DH / E;              // chunks of a row
+  static constexpr int ROW = DH * (int)sizeof(T);
+  static constexpr int KS = NC / 2;              // steps of a sum over DH
+  static constexpr int PS = 32 / (2 * E);        // steps of a sum over 32 rows
+  static constexpr int ND = DH / 32;
+
+  static __device__ __forceinline__ int swz(int r) {
+    if constexpr (NC == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    return ((r & 3) << 2) | ((r >> 2) & 3);
+  }
+  static __device__ __forceinline__ int at(int r, int chunk) { return r * ROW + ((chunk ^ swz(r)) << 4); }
+
+  // rows r0 .. r0+31, step s of the sum over DH: lane l holds chunk 2s + l/32 of row l%32
+  static __device__ __forceinline__ uint4 rows(const unsigned char *t, int r0, int s, int lane) {
+    return *reinterpret_cast<const uint4 *>(t + at(r0 + (lane & 31), 2 * s + (lane >> 5)));
+  }
+  // columns 32d .. 32d+31, step s of the sum over rows r0 .. r0+31, in the order in
+  // which a score register block holds them: lane l, column l%32, half h = l/32:
+  //   bf16: rows 16s + 8(i/4) + 4h + i%4, i = 0..7     fp32: rows 8s + 4h + i, i = 0..3
+  static __device__ __forceinline__ uint4 cols(const unsigned char *t, int r0, int s, int d, int lane) {
+    const int h = lane >> 5;
+    if constexpr (sizeof(T) == 2) {
+      const int r = r0 + 16 * s + 4 * h + ((lane & 15) >> 2);
+      const int chunk = 4 * d + ((lane >> 3) & 2) + ((lane >> 1) & 1), b = (lane & 1) << 3;
+      const uint2 lo = read_tr16(t + at(r, chunk) + b), hi = read_tr16(t + at(r + 8, chunk) + b);
+      return make_uint4(lo.x, lo.y, hi.x, hi.y);
+    } else {
+      const int r = r0 + 8 * s + 4 * h, chunk = 8 * d + ((lane & 31) >> 2), b = (lane & 3) << 2;
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t *>(t + at(r + i, chunk) + b);
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  // one element
+  static __device__ __forceinline__ float elem(const unsigned char *t, int r, int col) {
+    return to_f32(*reinterpret_cast<const T *>(t + at(r, col / E) + (col % E) * (int)sizeof(T)));
+  }
+};
+
+// Score registers as the B operand of a sum over the streamed rows, step s
+// (rounded to bf16 to nearest even for the bf16 matrix cores).
+template <typename T>
+__device__ __forceinline__ uint4 score_frag(const f32x16 &p, int s) {
+  if constexpr (sizeof(T) == 2) {
+    bf16x8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (bf16)p[8 * s + i];
+    return __builtin_bit_cast(uint4, r);
+  } else {
+    return make_uint4(__float_as_uint(p[4 * s]), __float_as_uint(p[4 * s + 1]), __float_as_uint(p[4 * s + 2]),
+                      __float_as_uint(p[4 * s + 3]));
+  }
+}
+// streamed row (of 32) that register i of a score block holds in half h
+__device__ __forceinline__ int score_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
+
+// Copies rows [row0, row0 + ROWS) of one head into a tile, through registers:
+// fetch() issues the loads, store() writes what came.  Rows at or past `limit`
+// and elements past head_dim come as zeros.
+template <typename T, int DH, int ROWS, int THREADS>
+struct Stage {
+  using TL = Tile<T, DH>;
+  static constexpr int N = ROWS * TL::NC / THREADS;
+  static_assert(ROWS * TL::NC % THREADS == 0, "");
+  uint4 r[N];
+  __device__ __forceinline__ void fetch(const char *head, int64_t row_bytes, int row0, int limit, int hd, int tid) {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(head + (int64_t)row0 * row_bytes, kOutside);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = i * THREADS + tid, row = x / TL::NC, chunk = x % TL::NC;
+      const bool in = row0 + row < limit && chunk * TL::E < hd;
+      r[i] = buf_load16(rs, in ? (uint32_t)row * (uint32_t)row_bytes + chunk * 16u : kOutside);
+    }
+  }
+  __device__ __forceinline__ void store(unsigned char *t, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = i * THREADS + tid;
+      *reinterpret_cast<uint4 *>(t + TL::at(x / TL::NC, x % TL::NC)) = r[i];
+    }
+  }
+};
+
+// A chunk of an owned row straight from memory (zeros past head_dim or when
+// the row is not there).
+template <typename T, int DH>
+__device__ __forceinline__ uint4 owned_chunk(const char *row, bool there, int chunk, int hd) {
+  if (!there || chunk * Tile<T, DH>::E >= hd) return make_uint4(0, 0, 0, 0);
+  return *reinterpret_cast<const uint4 *>(row + chunk * 16);
+}
+
+// Whether rows r0 .. r0+31 of a tile hold an infinity or a NaN (uniform).
+template <typename T, int DH>
+__device__ __forceinline__ bool not_finite(const unsigned char *t, int r0, int lane) {
+  float z = 0.f;
+#pragma unroll
+  for (int s = 0; s < Tile<T, DH>::KS; ++s) {
+    float f[Tile<T, DH>::E];
+    widen<T>(Tile<T, DH>::rows(t, r0, s, lane), f);
+#pragma unroll
+    for (int i = 0; i < Tile<T, DH>::E; ++i) z = __builtin_fmaf(f[i], 0.f, z);  // 0, or NaN from then on
+  }
+  return __ballot(!(z == 0.f)) != 0;
+}
+
+// A fragment with its infinities and NaN replaced by zeros.
+template <typename T>
+__device__ __forceinline__ uint4 finite_part(const uint4 &x) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+      if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+    } else {
+      if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] = 0;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// acc[column][owned row] += p[row] tile[row][column] for the infinities and NaN of
+// rows r0 .. r0+31 alone, where bit i of `seen` (register i of p) is set.
+template <typename T, int DH>
+__device__ __forceinline__ void add_seen(const unsigned char *t, int r0, f32x16 p, uint32_t seen,
+                                         f32x16 (&acc)[DH / 32], int lane) {
+  const int h = lane >> 5;
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) {
+    const float own = p[0];
+#pragma unroll
+    for (int k = 0; k < 15; ++k) p[k] = p[k + 1];  // (registers are not indexed by a variable)
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      // the p of row score_row(i, half) lies in the lanes of that half
+      const int from = (lane & 31) + 32 * half;
+      const float pr = __shfl(own, from);
+      const bool see = ((uint32_t)__shfl((int)seen, from) >> i & 1u) != 0;
+      const int row = r0 + score_row(i, half);
+#pragma unroll
+      for (int d = 0; d < DH / 32; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float x = Tile<T, DH>::elem(t, row, 32 * d + score_row(j, h));
+          if (see && !(__builtin_fabsf(x) < INFINITY)) acc[d][j] = __builtin_fmaf(pr, x, acc[d][j]);
+        }
+    }
+  }
+}
+
+// acc += tile^T p over rows r0 .. r0+31.  `guard`: some row is not seen by some
+// owned row.  A product with its zero p would carry an infinity or a NaN there, so
+// these are then taken out of the product and added only where they are seen; the
+// sum of everything else keeps its order, bit for bit.
+template <typename T, int DH>
+__device__ __forceinline__ void sum_rows(const unsigned char *t, int r0, const f32x16 &p, bool guard, uint32_t seen,
+                                         f32x16 (&acc)[DH / 32], int lane) {
+  using TL = Tile<T, DH>;
+  if (guard && not_finite<T, DH>(t, r0, lane)) {
+#pragma unroll
+    for (int s = 0; s < TL::PS; ++s) {
+      const uint4 b = score_frag<T>(p, s);
+#pragma unroll
+      for (int d = 0; d < TL::ND; ++d) mma_step<T>(finite_part<T>(TL::cols(t, r0, s, d, lane)), b, acc[d]);
+    }
+    add_seen<T, DH>(t, r0, p, seen, acc, lane);
+    return;
+  }
+#pragma unroll
+  for (int s = 0; s < TL::PS; ++s) {
+    const uint4 b = score_frag<T>(p, s);
+#pragma unroll
+    for (int d = 0; d < TL::ND; ++d) mma_step<T>(TL::cols(t, r0, s, d, lane), b, acc[d]);
+  }
+}
+
+// Writes an accumulator block acc[column][owned row] times f as a row of T.
+template <typename T, int DH>
+__device__ __forceinline__ void write_row(char *row, const f32x16 (&acc)[DH / 32], float f, int hd, int lane) {
+#pragma unroll
+  for (int d = 0; d < DH / 32; ++d)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int col = 32 * d + 8 * b + 4 * (lane >> 5);
+      if (col >= hd) continue;
+      if constexpr (sizeof(T) == 2) {
+        bf16 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = (bf16)(acc[d][4 * b + i] * f);
+        *reinterpret_cast<uint2 *>(row + col * 2) = __builtin_bit_cast(uint2, *(const u32x2 *)w);
+      } else {
+        *reinterpret_cast<float4 *>(row + col * 4) =
+            make_float4(acc[d][4 * b] * f, acc[d][4 * b + 1] * f, acc[d][4 * b + 2] * f, acc[d][4 * b + 3] * f);
+      }
+    }
+}
+
+// Blocks over (tile, head, batch row): the tiles with most work first, and,
+// where the heads divide among the 8 XCDs, a head's tiles on one XCD (block b
+// runs on XCD b % 8), so that its keys and values stay in that XCD's L2.
+__device__ __forceinline__ void block_of(int n_heads_all, int &tile_rank, int &head) {
+  const int b = blockIdx.x;
+  if (n_heads_all % 8 == 0) {
+    const int per = n_heads_all / 8, i = b >> 3;
+    head = (b & 7) * per + i % per;
+    tile_rank = i / per;
+  } else {
+    head = b % n_heads_all;
+    tile_rank = b / n_heads_all;
+  }
+}
+
+int attn_fwd(const AttnArgs &a, int dtype, hipStream_t st);
+int attn_bwd(const AttnArgs &a, int dtype, hipStream_t st);
+// blocks that share a key/value head's query heads in the dk/dv kernel, and the
+// partial sums this takes (fp32 elements; 0 with one block)
+int attn_bwd_splits(int64_t B, int64_t T, int H, int G);
+
+}  // namespace dynconv

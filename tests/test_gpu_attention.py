@@ -1,0 +1,242 @@
+"""Causal attention over whole sequences (dynconv_attn_fwd, dynconv_attn_bwd)
+against its fp64 definition: head layouts, odd lengths and widths, packed
+documents with empty and one-token ones and a padded end, views of one row and
+head-major views, infinities and NaN where a row does not look, gradients
+against differences, repeatability, replay in a HIP graph, two streams."""
+from __future__ import annotations
+
+import math
+import sys
+
+import pytest
+import torch
+
+import input_dependent_depthwise_amd as dc
+from tests import attn_util as au
+
+pytestmark = pytest.mark.gpu
+
+
+def _note(msg):
+    print(msg, flush=True)
+    sys.stdout.flush()
+
+
+def _row(B, T, H, G, hd, dtype, seed):
+    """q, k, v as the parts of one row, and d_o."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    dt = au.DTYPES[dtype]
+    row = torch.randn(B, T, H + 2 * G, hd, generator=g, device="cuda").to(dt)
+    d_o = torch.randn(B, T, H, hd, generator=g, device="cuda").to(dt)
+    return row[:, :, :H], row[:, :, H:H + G], row[:, :, H + G:], d_o
+
+
+def _run(q, k, v, d_o, cu=None, scale=None):
+    c = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    o, lse = dc.dynconv_attn_fwd(q, k, v, cu_seqlens=c, scale=scale, want_lse=True)
+    g = dc.dynconv_attn_bwd(q, k, v, o, lse, d_o, cu_seqlens=c, scale=scale)
+    torch.cuda.synchronize()
+    return {"o": o, "lse": lse, **g}
+
+
+def _compare(got, ref, dtype):
+    # (2^-20: fp32 sums of up to 128 products, 2^-24 each)
+    errs = {n: au.rel(got[n], ref[n], 2.0 ** -20 * ref.get("~" + n, 0.0)) for n in ref if n[0] != "~"}
+    assert all(e <= (1e-5 if n == "lse" else au.TOL[dtype]) for n, e in errs.items()), errs
+
+
+SHAPES = [
+    # B, T, H, G, hd
+    (1, 1, 1, 1, 64),
+    (2, 1, 4, 2, 128),
+    (1, 2, 3, 1, 16),
+    (1, 31, 2, 2, 64),
+    (2, 33, 4, 4, 16),
+    (1, 64, 2, 1, 128),
+    (3, 65, 6, 3, 80),
+    (1, 127, 8, 1, 96),
+    (1, 128, 8, 8, 8),
+    (2, 129, 4, 2, 64),
+    (1, 200, 7, 1, 128),
+    (2, 257, 2, 1, 24),
+    (1, 515, 12, 12, 64),
+    (1, 1030, 16, 4, 128),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_against_definition(shape, dtype):
+    _note(f"[attn] {shape} {dtype}")
+    q, k, v, d_o = _row(*shape, dtype, seed=sum(shape))
+    _compare(_run(q, k, v, d_o), au.attention(q, k, v, d_o=d_o), dtype)
+
+
+PACKED = [
+    # offsets, T (the rest of the row is padding)
+    ([0, 5], 5),
+    ([0, 0, 1, 1, 2, 40, 40], 40),
+    ([0, 31, 64, 65, 130], 130),
+    ([0, 100, 228, 300], 333),
+    ([0, 0, 0], 20),
+    ([0, 7, 7, 128, 129, 512, 700], 700),
+    ([0] + list(range(3, 600, 3)), 640),
+    ([0, 126, 1000], 1027),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("heads", [(4, 4, 64), (8, 2, 128), (3, 1, 40)], ids=str)
+@pytest.mark.parametrize("docs", PACKED, ids=[f"docs{i}" for i in range(len(PACKED))])
+def test_packed_documents(docs, heads, dtype):
+    cu, T = docs
+    H, G, hd = heads
+    _note(f"[attn] packed {len(cu) - 1} documents T={T} {heads} {dtype}")
+    q, k, v, d_o = _row(1, T, H, G, hd, dtype, seed=T + H)
+    got = _run(q, k, v, d_o, cu=cu)
+    _compare(got, au.attention(q, k, v, cu=cu, d_o=d_o), dtype)
+    for n in ("o", "dq", "dk", "dv"):  # tokens of no document: exact zeros
+        assert bool((got[n][:, cu[-1]:] == 0).all()), n
+    assert bool((got["lse"][:, :, cu[-1]:] == -math.inf).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_scale_and_large_scores(dtype):
+    """Scores of some hundreds: the running maximum moves often and most probabilities vanish."""
+    _note(f"[attn] large scores {dtype}")
+    q, k, v, d_o = _row(2, 300, 4, 2, 64, dtype, seed=5)
+    got, ref = _run(q, k, v, d_o, scale=6.0), au.attention(q, k, v, scale=6.0, d_o=d_o)
+    # scores of |s| <= 300 carry an absolute error of |s| 2^-23 or so (fp32 sums), which p takes on as
+    # a relative one, and near ties do.v - delta cancels
+    for n in got:
+        assert au.rel(got[n], ref[n]) <= (1e-5 if n == "lse" else au.TOL["bf16"] if dtype == "bf16" else 2e-4), n
+
+
+def test_views():
+    """Head-major tensors, heads shared by stride 0, gradients into the parts of one row: bitwise as for plain tensors."""
+    _note("[attn] views")
+    q, k, v, d_o = _row(2, 150, 4, 2, 64, "bf16", seed=9)
+    ref = _run(q.contiguous(), k.contiguous(), v.contiguous(), d_o)
+    hm = lambda t: t.transpose(1, 2).contiguous().transpose(1, 2)  # noqa: E731  [B, heads, T, head_dim] in memory
+    got = _run(hm(q), hm(k), hm(v), hm(d_o))
+    assert all(torch.equal(got[n], ref[n]) for n in ref)
+    row = torch.full((2, 150, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = {"dq": row[:, :, :4], "dk": row[:, :, 4:6], "dv": row[:, :, 6:]}
+    dc.dynconv_attn_bwd(q, k, v, ref["o"], ref["lse"], d_o, out=out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out[n], ref[n]) for n in out)
+    one_k, one_v = k[:, :, :1].expand(-1, -1, 2, -1), v[:, :, :1].expand(-1, -1, 2, -1)
+    got = _run(q, one_k, one_v, d_o)
+    ref = _run(q, one_k.contiguous(), one_v.contiguous(), d_o)
+    assert all(torch.equal(got[n], ref[n]) for n in ref)
+
+
+BAD = [math.inf, -math.inf, math.nan, 3.0e38]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("bad", BAD, ids=str)
+def test_masked_places_do_not_reach(bad, hd, dtype):
+    """One document, the padding and the later tokens of a row hold what would spoil a product with a zero."""
+    _note(f"[attn] {bad} in masked places {hd} {dtype}")
+    cu, T = [0, 40, 75, 170], 200
+    q, k, v, d_o = _row(1, T, 4, 2, hd, dtype, seed=13)
+    want = _run(q, k, v, d_o, cu=cu)
+    q2, k2, v2, d2 = (t.clone() for t in (q, k, v, d_o))
+    for t in (q2, k2, v2, d2):
+        t[:, 40:75] = bad    # the second document
+        t[:, 170:] = bad     # the padding
+    got = _run(q2, k2, v2, d2, cu=cu)
+    for n in ("o", "dq", "dk", "dv"):
+        assert torch.equal(got[n][:, :40], want[n][:, :40]), n
+        assert torch.equal(got[n][:, 75:170], want[n][:, 75:170]), n
+        assert bool((got[n][:, 170:] == 0).all()), n
+    # later tokens: rows before them see nothing of it
+    v3, k3 = v.clone(), k.clone()
+    v3[:, 20:40] = bad
+    k3[:, 20:40] = bad
+    got = _run(q, k3, v3, d_o, cu=cu)
+    assert torch.equal(got["o"][:, :20], want["o"][:, :20])
+    assert torch.equal(got["dq"][:, :20], want["dq"][:, :20])
+
+
+def test_gradients_against_differences():
+    """Central differences of sum(o * d_o) along random directions (fp32 outputs, fp64 sums, step 1/64:
+    truncation of order step^2, rounding 2^-24 / step)."""
+    _note("[attn] differences")
+    q, k, v, d_o = (t.contiguous() for t in _row(1, 90, 4, 2, 32, "fp32", seed=21))
+    cu = [0, 33, 90]
+    g = _run(q, k, v, d_o, cu=cu)
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(22)
+    step = 1 / 64
+    for name, i in (("dq", 0), ("dk", 1), ("dv", 2)):
+        x = [q, k, v]
+        d = torch.randn(x[i].shape, generator=gen, device="cuda")
+
+        def loss(sign):
+            y = list(x)
+            y[i] = x[i] + sign * step * d
+            return (dc.dynconv_attn_fwd(*y, cu_seqlens=c).double() * d_o.double()).sum()
+
+        num = ((loss(1) - loss(-1)) / (2 * step)).item()
+        ana = (g[name].double() * d.double()).sum().item()
+        size = g[name].double().norm().item() * math.sqrt(d.numel()) / math.sqrt(g[name].numel()) + 1.0
+        assert abs(num - ana) <= 1e-2 * size, (name, num, ana, size)
+
+
+def test_repeatable_and_on_two_streams():
+    _note("[attn] repeat, two streams")
+    q, k, v, d_o = _row(2, 700, 8, 2, 128, "bf16", seed=31)
+    ref = _run(q, k, v, d_o)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        out = []
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                o, lse = dc.dynconv_attn_fwd(q, k, v, want_lse=True)
+                out.append({"o": o, "lse": lse, **dc.dynconv_attn_bwd(q, k, v, o, lse, d_o)})
+        torch.cuda.synchronize()
+        for got in out:
+            assert all(torch.equal(got[n], ref[n]) for n in ref)
+
+
+def test_graph_replay():
+    _note("[attn] graph")
+    q, k, v, d_o = (t.contiguous() for t in _row(1, 333, 4, 2, 64, "bf16", seed=41))
+    c = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+
+    def step():
+        o, lse = dc.dynconv_attn_fwd(q, k, v, cu_seqlens=c, want_lse=True)
+        return {"o": o, "lse": lse, **dc.dynconv_attn_bwd(q, k, v, o, lse, d_o, cu_seqlens=c)}
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for r in range(3):
+        for t, n in zip((q, k, v, d_o), _row(1, 333, 4, 2, 64, "bf16", seed=50 + r)):
+            t.copy_(n)
+        c.copy_(torch.tensor([0, 60 + r, 333 - r], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[n], eager[n]) for n in eager), r
+
+
+def test_empty():
+    q = torch.empty(0, 5, 4, 64, dtype=torch.bfloat16, device="cuda")
+    assert dc.dynconv_attn_fwd(q, q, q).shape == q.shape
+    q = torch.empty(2, 0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = dc.dynconv_attn_fwd(q, q, q, want_lse=True)
+    g = dc.dynconv_attn_bwd(q, q, q, o, lse, q)
+    torch.cuda.synchronize()
+    assert lse.shape == (2, 4, 0) and g["dk"].shape == q.shape
