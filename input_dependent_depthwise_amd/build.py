@@ -35,6 +35,9 @@ CFLAGS = [
 # accumulating in the matrix cores are better off with AGPR accumulators.
 FILE_FLAGS = {
     "conv_fwd_lowrank.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    # one wave per SIMD holds more than 256 registers here: without it every score block is copied
+    # between the two halves of the register file
+    "attn_bwd_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

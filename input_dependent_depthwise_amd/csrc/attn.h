@@ -209,88 +209,113 @@ __device__ __forceinline__ uint4 owned_chunk(const char *row, bool there, int ch
   return *reinterpret_cast<const uint4 *>(row + chunk * 16);
 }
 
-// Whether rows r0 .. r0+31 of a tile hold an infinity or a NaN (uniform).
-template <typename T, int DH>
-__device__ __forceinline__ bool not_finite(const unsigned char *t, int r0, int lane) {
-  float z = 0.f;
-#pragma unroll
-  for (int s = 0; s < Tile<T, DH>::KS; ++s) {
-    float f[Tile<T, DH>::E];
-    widen<T>(Tile<T, DH>::rows(t, r0, s, lane), f);
-#pragma unroll
-    for (int i = 0; i < Tile<T, DH>::E; ++i) z = __builtin_fmaf(f[i], 0.f, z);  // 0, or NaN from then on
-  }
-  return __ballot(!(z == 0.f)) != 0;
-}
-
-// A fragment with its infinities and NaN replaced by zeros.
-template <typename T>
-__device__ __forceinline__ uint4 finite_part(const uint4 &x) {
+// Elements of a fragment replaced: `KEEP` its finite ones with zeros for the rest,
+// `SIGN` the sign of its infinities and zeros for the rest, `ONE` ones for
+// infinities and NaN and zeros for the rest.
+enum class Part { KEEP, SIGN, ONE };
+template <typename T, Part P>
+__device__ __forceinline__ uint4 part_of(const uint4 &x) {
   uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (sizeof(T) == 2) {
-      if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
-      if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+      uint32_t r = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t v = w[i] >> (16 * k) & 0xffffu;
+        const bool fin = (v & 0x7f80u) != 0x7f80u, inf = (v & 0x7fffu) == 0x7f80u;
+        const uint32_t n = P == Part::KEEP ? (fin ? v : 0u)
+                           : P == Part::SIGN ? (inf ? (v & 0x8000u) | 0x3f80u : 0u) : (fin ? 0u : 0x3f80u);
+        r |= n << (16 * k);
+      }
+      w[i] = r;
     } else {
-      if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] = 0;
+      const uint32_t v = w[i];
+      const bool fin = (v & 0x7f800000u) != 0x7f800000u, inf = (v & 0x7fffffffu) == 0x7f800000u;
+      w[i] = P == Part::KEEP ? (fin ? v : 0u)
+             : P == Part::SIGN ? (inf ? (v & 0x80000000u) | 0x3f800000u : 0u) : (fin ? 0u : 0x3f800000u);
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// acc[column][owned row] += p[row] tile[row][column] for the infinities and NaN of
-// rows r0 .. r0+31 alone, where bit i of `seen` (register i of p) is set.
+// Whether rows r0 .. r0+31 of a tile hold an infinity or a NaN (uniform).
 template <typename T, int DH>
-__device__ __forceinline__ void add_seen(const unsigned char *t, int r0, f32x16 p, uint32_t seen,
-                                         f32x16 (&acc)[DH / 32], int lane) {
-  const int h = lane >> 5;
-#pragma unroll 1
+__device__ __forceinline__ bool not_finite(const unsigned char *t, int r0, int lane) {
+  using TL = Tile<T, DH>;
+  uint32_t any = 0;
+#pragma unroll
+  for (int s = 0; s < TL::PS; ++s)
+#pragma unroll
+    for (int d = 0; d < TL::ND; ++d) {
+      const uint4 x = part_of<T, Part::ONE>(TL::cols(t, r0, s, d, lane));
+      any |= x.x | x.y | x.z | x.w;
+    }
+  return __ballot(any != 0) != 0;
+}
+
+// acc += tile^T p over rows r0 .. r0+31 of which some hold an infinity or a NaN:
+// the product of the finite values, as ever and bit for bit, then what the
+// others make of the sums of the owned rows that see them.  With S the sum
+// of sign(value) sign(p) over seen infinities and Q the count of seen
+// infinities and NaN, both products as well: nothing for Q = 0, +infinity for
+// S = Q, -infinity for S = -Q, else NaN.
+template <typename T, int DH>
+__device__ __forceinline__ void sum_rows_guarded(const unsigned char *t, int r0, const f32x16 &p, uint32_t seen,
+                                                 f32x16 (&acc)[DH / 32], int lane) {
+  using TL = Tile<T, DH>;
+  f32x16 one, sign;
+#pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float own = p[0];
+    one[i] = seen >> i & 1u ? 1.f : 0.f;
+    sign[i] = p[i] > 0.f ? one[i] : p[i] < 0.f ? -one[i] : 0.f;
+  }
 #pragma unroll
-    for (int k = 0; k < 15; ++k) p[k] = p[k + 1];  // (registers are not indexed by a variable)
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      // the p of row score_row(i, half) lies in the lanes of that half
-      const int from = (lane & 31) + 32 * half;
-      const float pr = __shfl(own, from);
-      const bool see = ((uint32_t)__shfl((int)seen, from) >> i & 1u) != 0;
-      const int row = r0 + score_row(i, half);
+  for (int d = 0; d < TL::ND; ++d) {
+    f32x16 sum, count;
 #pragma unroll
-      for (int d = 0; d < DH / 32; ++d)
+    for (int i = 0; i < 16; ++i) sum[i] = count[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float x = Tile<T, DH>::elem(t, row, 32 * d + score_row(j, h));
-          if (see && !(__builtin_fabsf(x) < INFINITY)) acc[d][j] = __builtin_fmaf(pr, x, acc[d][j]);
-        }
+    for (int s = 0; s < TL::PS; ++s) {
+      const uint4 x = TL::cols(t, r0, s, d, lane);
+      mma_step<T>(part_of<T, Part::KEEP>(x), score_frag<T>(p, s), acc[d]);
+      mma_step<T>(part_of<T, Part::SIGN>(x), score_frag<T>(sign, s), sum);
+      mma_step<T>(part_of<T, Part::ONE>(x), score_frag<T>(one, s), count);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float with = acc[d][i] + (sum[i] == count[i] ? INFINITY : sum[i] == -count[i] ? -INFINITY : NAN);
+      acc[d][i] = count[i] != 0.f ? with : acc[d][i];
     }
   }
 }
 
-// acc += tile^T p over rows r0 .. r0+31.  `guard`: some row is not seen by some
-// owned row.  A product with its zero p would carry an infinity or a NaN there, so
-// these are then taken out of the product and added only where they are seen; the
-// sum of everything else keeps its order, bit for bit.
+// acc += tile^T p over rows r0 .. r0+31.
 template <typename T, int DH>
-__device__ __forceinline__ void sum_rows(const unsigned char *t, int r0, const f32x16 &p, bool guard, uint32_t seen,
-                                         f32x16 (&acc)[DH / 32], int lane) {
+__device__ __forceinline__ void sum_rows(const unsigned char *t, int r0, const f32x16 &p, f32x16 (&acc)[DH / 32],
+                                         int lane) {
   using TL = Tile<T, DH>;
-  if (guard && not_finite<T, DH>(t, r0, lane)) {
-#pragma unroll
-    for (int s = 0; s < TL::PS; ++s) {
-      const uint4 b = score_frag<T>(p, s);
-#pragma unroll
-      for (int d = 0; d < TL::ND; ++d) mma_step<T>(finite_part<T>(TL::cols(t, r0, s, d, lane)), b, acc[d]);
-    }
-    add_seen<T, DH>(t, r0, p, seen, acc, lane);
-    return;
-  }
 #pragma unroll
   for (int s = 0; s < TL::PS; ++s) {
     const uint4 b = score_frag<T>(p, s);
 #pragma unroll
     for (int d = 0; d < TL::ND; ++d) mma_step<T>(TL::cols(t, r0, s, d, lane), b, acc[d]);
+  }
+}
+
+// In a tile where some row is not seen by some owned row, a product with that pair's zero p would
+// carry an infinity or a NaN of the row to where it is not seen.  A kernel's first
+// pass (GUARD false) only notes that it met one in such a tile; its block then starts
+// over with GUARD, where such tiles take sum_rows_guarded.  (Both in one loop would keep the
+// registers of the rare path from the common one.)
+template <bool GUARD, typename T, int DH>
+__device__ __forceinline__ void sum_rows_masked(const unsigned char *t, int r0, const f32x16 &p, uint32_t seen,
+                                                f32x16 (&acc)[DH / 32], bool &met, int lane) {
+  if constexpr (GUARD) {
+    if (not_finite<T, DH>(t, r0, lane)) sum_rows_guarded<T, DH>(t, r0, p, seen, acc, lane);
+    else sum_rows<T, DH>(t, r0, p, acc, lane);
+  } else {
+    met |= not_finite<T, DH>(t, r0, lane);
   }
 }
 
@@ -332,6 +357,7 @@ __device__ __forceinline__ void block_of(int n_heads_all, int &tile_rank, int &h
 
 int attn_fwd(const AttnArgs &a, int dtype, hipStream_t st);
 int attn_bwd(const AttnArgs &a, int dtype, hipStream_t st);
+int attn_bwd_fp32(const AttnArgs &a, hipStream_t st);
 // blocks that share a key/value head's query heads in the dk/dv kernel, and the
 // partial sums this takes (fp32 elements; 0 with one block)
 int attn_bwd_splits(int64_t B, int64_t T, int H, int G);

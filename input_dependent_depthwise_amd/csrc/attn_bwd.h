@@ -1,0 +1,405 @@
+// attn_bwd.h -- causal attention over whole sequences, backward: the kernels
+// (compiled by attn_bwd_bf16.hip and attn_bwd_fp32.hip).
+//
+// Two kernels, neither with atomics: dq with queries owned by the lanes and
+// keys streamed (it also forms delta = do . o), then dk and dv with keys owned
+// and queries streamed.  The scores are formed twice (7 products where 5 would
+// do), which costs less than a fixed-order sum of dq over blocks of keys.
+#pragma once
+
+#include "attn.h"
+#include "kernels.h"
+
+namespace dynconv {
+
+namespace {
+
+template <typename T, int DH, int BN>
+struct Dq {
+  using TL = Tile<T, DH>;
+  typedef unsigned char Lds[2][2][BN * TL::ROW];  // [buffer][key, value]
+  // the block: keys of its head, their range, valid tokens
+  const char *kh, *vh;
+  int64_t krow, vrow;
+  int q0, first, last, limit, hd;
+  // the wave: its first query, first key, and the key from which on every row sees keys
+  int qw, w_first, w_full;
+  int q, start;  // the lane's query and its document's start
+  float c;       // scale log2 e
+  float lse2, delta;
+  uint4 qf[TL::KS], df[TL::KS];
+  f32x16 acc[TL::ND];
+
+  __device__ __forceinline__ void scores(const unsigned char *kl, const unsigned char *vl, int n, f32x16 &p,
+                                         f32x16 &dp, int lane) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = dp[i] = 0.f;
+#pragma unroll
+    for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(kl, 32 * n, s, lane), qf[s], p);
+#pragma unroll
+    for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(vl, 32 * n, s, lane), df[s], dp);
+  }
+
+  // delta = sum_j p (do . v_j) over the keys from the block's first query on.
+  __device__ __forceinline__ float delta_of_block(Lds &lds, int tid, int lane) const {
+    const int h = lane >> 5;
+    Stage<T, DH, BN, 256> sk, sv;
+    float sum = 0.f;
+    for (int kt = q0; kt <= last; kt += BN) {
+      sk.fetch(kh, krow, kt, limit, hd, tid);
+      sv.fetch(vh, vrow, kt, limit, hd, tid);
+      sk.store(lds[0][0], tid);
+      sv.store(lds[0][1], tid);
+      __syncthreads();
+#pragma unroll 1
+      for (int n = 0; n < BN / 32; ++n) {
+        f32x16 p, dp;
+        scores(lds[0][0], lds[0][1], n, p, dp, lane);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = kt + 32 * n + score_row(i, h);
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -lse2)) * dp[i];
+          if (key <= q && key >= start) sum += x;
+        }
+      }
+      __syncthreads();
+    }
+    return half_sum(sum);
+  }
+
+  // All keys of the block; whether an infinity or a NaN in a masked tile was met (GUARD: never).
+  template <bool GUARD>
+  __device__ __forceinline__ bool pass(Lds &lds, int tid, int lane) {
+    const int h = lane >> 5;
+    bool met = false;
+#pragma unroll
+    for (int d = 0; d < TL::ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
+    Stage<T, DH, BN, 256> sk, sv;
+    int buf = 0;
+    if (first <= last) {
+      sk.fetch(kh, krow, first, limit, hd, tid);
+      sv.fetch(vh, vrow, first, limit, hd, tid);
+      sk.store(lds[0][0], tid);
+      sv.store(lds[0][1], tid);
+    }
+    __syncthreads();
+    for (int kt = first; kt <= last; kt += BN) {
+      const bool more = kt + BN <= last;
+      if (more) {
+        sk.fetch(kh, krow, kt + BN, limit, hd, tid);
+        sv.fetch(vh, vrow, kt + BN, limit, hd, tid);
+      }
+      if (kt <= qw + 31 && kt + BN > w_first && qw < limit) {
+        const unsigned char *kl = lds[buf][0], *vl = lds[buf][1];
+        const bool masked = kt + BN - 1 > qw || kt < w_full;
+#pragma unroll
+        for (int n = 0; n < BN / 32; ++n) {
+          f32x16 p, dp;
+          scores(kl, vl, n, p, dp, lane);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -lse2)) * (dp[i] - delta);
+          if (masked) {
+            uint32_t seen = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int key = kt + 32 * n + score_row(i, h);
+              const bool see = key <= q && key >= start;
+              if (!see) p[i] = 0.f;
+              seen |= (uint32_t)see << i;
+            }
+            sum_rows_masked<GUARD, T, DH>(kl, 32 * n, p, seen, acc, met, lane);
+          }
+          if (!GUARD || !masked) sum_rows<T, DH>(kl, 32 * n, p, acc, lane);
+        }
+      }
+      if (more) {
+        sk.store(lds[buf ^ 1][0], tid);
+        sv.store(lds[buf ^ 1][1], tid);
+      }
+      __syncthreads();
+      buf ^= 1;
+    }
+    return met;
+  }
+};
+
+template <typename T, int DH, int BN>
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
+  using F = Dq<T, DH, BN>;
+  using TL = Tile<T, DH>;
+  __shared__ __align__(16) typename F::Lds lds;
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
+  int rank, bh;
+  block_of(a.B * a.H, rank, bh);
+  const int n_tiles = (a.T + 127) / 128;
+  const int b = bh / a.H, e = bh % a.H, g = e / (a.H / a.G);
+  F f;
+  f.q0 = (n_tiles - 1 - rank) * 128;
+  f.kh = a.k.p + b * a.k.batch + g * a.k.head;
+  f.vh = a.v.p + b * a.v.batch + g * a.v.head;
+  f.krow = a.k.row;
+  f.vrow = a.v.row;
+  f.hd = a.hd;
+  f.c = a.scale * kLog2e;
+  f.qw = f.q0 + wave * 32;
+  f.limit = uniform(tokens_in_docs(a.cu, a.n_seqs, a.T));
+  const int q = f.qw + (lane & 31);
+  f.q = q;
+  int tail, unused;  // tail: where the document of the block's last token starts
+  doc_of(a.cu, a.n_seqs, a.T, q, f.start, unused);
+  doc_of(a.cu, a.n_seqs, a.T, f.q0, f.first, unused);
+  f.first = uniform(f.first);
+  f.last = min(f.q0 + 127, f.limit - 1);
+  doc_of(a.cu, a.n_seqs, a.T, f.last, tail, unused);
+  tail = uniform(tail);
+  f.w_first = uniform(f.start);  // (lane 0 has the lowest start)
+  f.w_full = __builtin_amdgcn_readlane(f.start, 31);
+
+  // a token of no document contributes nothing, whatever its rows hold
+  const bool there = q < f.limit;
+  const char *qrow = a.q.p + b * a.q.batch + e * a.q.head + (int64_t)q * a.q.row;
+  const char *drow = a.d_o.p + b * a.d_o.batch + e * a.d_o.head + (int64_t)q * a.d_o.row;
+  const char *orow = a.o.p + b * a.o.batch + e * a.o.head + (int64_t)q * a.o.row;
+  f.delta = 0.f;
+#pragma unroll
+  for (int s = 0; s < TL::KS; ++s) {
+    f.qf[s] = owned_chunk<T, DH>(qrow, there, 2 * s + h, a.hd);
+    f.df[s] = owned_chunk<T, DH>(drow, there, 2 * s + h, a.hd);
+    float x[TL::E], y[TL::E];
+    widen<T>(f.df[s], x);
+    widen<T>(owned_chunk<T, DH>(orow, there, 2 * s + h, a.hd), y);
+#pragma unroll
+    for (int i = 0; i < TL::E; ++i) f.delta = __builtin_fmaf(x[i], y[i], f.delta);
+  }
+  f.delta = half_sum(f.delta);
+  f.lse2 = INFINITY;  // log2 of the row's sum; +infinity: no key, every p is 0
+  if (there) {
+    const float v = a.lse[(int64_t)bh * a.T + q];
+    if (v != -INFINITY) f.lse2 = v * kLog2e;
+  }
+  // Rows with few keys take delta = sum_j p (do . v_j) instead: o carries a rounding (2^-8 with
+  // bf16) that ds = p (do . v - delta) does not forgive where a few keys share the weight (two
+  // tokens of head_dim 16: dq 1.2 % off), while over many keys |o| falls below |v| and the
+  // error with it.  Done for rows whose document starts in the block (at most 128 keys),
+  // which costs blocks without such a start nothing.
+  if (f.first <= f.last && tail >= f.q0) {
+    const float d = f.delta_of_block(lds, tid, lane);
+    if (f.start >= f.q0) f.delta = d;
+  }
+  if (q < a.T && h == 0) a.delta[(int64_t)bh * a.T + q] = f.delta;
+
+  const bool met = f.template pass<false>(lds, tid, lane);
+  if (__builtin_expect(__syncthreads_or(met), 0)) f.template pass<true>(lds, tid, lane);
+  if (q < a.T)
+    write_row<T, DH>(a.dq.p + b * a.dq.batch + e * a.dq.head + (int64_t)q * a.dq.row, f.acc, a.scale, a.hd, lane);
+}
+
+template <typename T, int DH, int BN>
+struct Dkv {
+  using TL = Tile<T, DH>;
+  struct Lds {
+    unsigned char tile[2][2][BN * TL::ROW];  // [buffer][query, do]
+    float stat[2][2][BN];                    // log2 of each query's sum (+infinity: no key), its delta
+  };
+  const AttnArgs &a;
+  int b, e0, per;        // batch row, first query head, query heads
+  int k0, stop, limit;   // the block: its first key, the last query + 1 that sees any, valid tokens
+  int kw, w_end;         // the wave: its first key; up to w_end every key is seen
+  int key, end;          // the lane's key and its document's end
+  float c;               // scale log2 e
+  uint4 kf[TL::KS], vf[TL::KS];
+  f32x16 ak[TL::ND], av[TL::ND];
+
+  // All (head, query tile) pairs of the block, heads outside; returns as Dq::pass.
+  template <bool GUARD>
+  __device__ __forceinline__ bool pass(Lds &lds, int tid, int lane) {
+    const int h = lane >> 5;
+    bool met = false;
+#pragma unroll
+    for (int d = 0; d < TL::ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ak[d][i] = av[d][i] = 0.f;
+    Stage<T, DH, BN, 256> sq, sd;
+    float st = 0.f;
+    auto fetch = [&](int e, int qt) {
+      sq.fetch(a.q.p + b * a.q.batch + e * a.q.head, a.q.row, qt, limit, a.hd, tid);
+      sd.fetch(a.d_o.p + b * a.d_o.batch + e * a.d_o.head, a.d_o.row, qt, limit, a.hd, tid);
+      if (tid < 2 * BN) {
+        const int which = tid / BN, i = qt + tid % BN;
+        const int64_t at = ((int64_t)b * a.H + e) * a.T + i;
+        if (which == 0) {
+          const float v = i < limit ? a.lse[at] : -INFINITY;
+          st = v == -INFINITY ? INFINITY : v * kLog2e;
+        } else {
+          st = i < limit ? a.delta[at] : 0.f;
+        }
+      }
+    };
+    auto store = [&](int to) {
+      sq.store(lds.tile[to][0], tid);
+      sd.store(lds.tile[to][1], tid);
+      if (tid < 2 * BN) lds.stat[to][tid / BN][tid % BN] = st;
+    };
+    const int n_all = k0 < stop ? (stop - k0 + BN - 1) / BN * per : 0;
+    int buf = 0;
+    if (n_all > 0) {
+      fetch(e0, k0);
+      store(0);
+    }
+    __syncthreads();
+    int e = e0, qt = k0;
+    for (int it = 0; it < n_all; ++it) {
+      int e2 = e, qt2 = qt + BN;
+      if (qt2 >= stop) {
+        qt2 = k0;
+        ++e2;
+      }
+      const bool more = it + 1 < n_all;
+      if (more) fetch(e2, qt2);
+      if (qt + BN > kw && kw < limit) {
+        const unsigned char *ql = lds.tile[buf][0], *dl = lds.tile[buf][1];
+        const bool masked = qt < kw + 31 || qt + BN > w_end;
+#pragma unroll
+        for (int n = 0; n < BN / 32; ++n) {
+          f32x16 p, dp;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] = dp[i] = 0.f;
+#pragma unroll
+          for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(ql, 32 * n, s, lane), kf[s], p);
+#pragma unroll
+          for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(dl, 32 * n, s, lane), vf[s], dp);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 l4 = *reinterpret_cast<const float4 *>(&lds.stat[buf][0][32 * n + 8 * j + 4 * h]);
+            const float4 d4 = *reinterpret_cast<const float4 *>(&lds.stat[buf][1][32 * n + 8 * j + 4 * h]);
+            const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, de[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              p[4 * j + i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[4 * j + i], c, -ls[i]));
+              dp[4 * j + i] = p[4 * j + i] * (dp[4 * j + i] - de[i]);
+            }
+          }
+          if (masked) {
+            uint32_t seen = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int q = qt + 32 * n + score_row(i, h);
+              const bool see = q >= key && q < end;
+              if (!see) p[i] = dp[i] = 0.f;
+              seen |= (uint32_t)see << i;
+            }
+            sum_rows_masked<GUARD, T, DH>(dl, 32 * n, p, seen, av, met, lane);
+            sum_rows_masked<GUARD, T, DH>(ql, 32 * n, dp, seen, ak, met, lane);
+          }
+          if (!GUARD || !masked) {
+            sum_rows<T, DH>(dl, 32 * n, p, av, lane);
+            sum_rows<T, DH>(ql, 32 * n, dp, ak, lane);
+          }
+        }
+      }
+      if (more) store(buf ^ 1);
+      __syncthreads();
+      buf ^= 1;
+      e = e2;
+      qt = qt2;
+    }
+    return met;
+  }
+};
+
+template <typename T, int DH, int BN>
+__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a) {
+  using F = Dkv<T, DH, BN>;
+  using TL = Tile<T, DH>;
+  __shared__ __align__(16) typename F::Lds lds;
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
+  const int group = a.H / a.G;  // query heads of a key/value head
+  int rank, bg;
+  block_of(a.B * a.G * a.n_split, rank, bg);
+  const int b = bg / (a.G * a.n_split), gs = bg % (a.G * a.n_split), g = gs / a.n_split, split = gs % a.n_split;
+  F f{a};
+  f.b = b;
+  f.per = group / a.n_split;
+  f.e0 = g * group + split * f.per;
+  f.k0 = rank * 128;
+  f.c = a.scale * kLog2e;
+  f.kw = f.k0 + wave * 32;
+  f.limit = uniform(tokens_in_docs(a.cu, a.n_seqs, a.T));
+  const int key = f.kw + (lane & 31);
+  f.key = key;
+  int unused;
+  doc_of(a.cu, a.n_seqs, a.T, key, unused, f.end);
+  doc_of(a.cu, a.n_seqs, a.T, min(f.k0 + 127, f.limit - 1), unused, f.stop);
+  f.stop = uniform(f.k0 < f.limit ? f.stop : 0);
+  f.w_end = __builtin_amdgcn_readlane(f.end, 0);  // (the wave's ends rise)
+
+  const bool there = key < f.limit;
+  const char *krow = a.k.p + b * a.k.batch + g * a.k.head + (int64_t)key * a.k.row;
+  const char *vrow = a.v.p + b * a.v.batch + g * a.v.head + (int64_t)key * a.v.row;
+#pragma unroll
+  for (int s = 0; s < TL::KS; ++s) {
+    f.kf[s] = owned_chunk<T, DH>(krow, there, 2 * s + h, a.hd);
+    f.vf[s] = owned_chunk<T, DH>(vrow, there, 2 * s + h, a.hd);
+  }
+  const bool met = f.template pass<false>(lds, tid, lane);
+  if (__builtin_expect(__syncthreads_or(met), 0)) f.template pass<true>(lds, tid, lane);
+  if (key >= a.T) return;
+  if (a.n_split == 1) {
+    write_row<T, DH>(a.dk.p + b * a.dk.batch + g * a.dk.head + (int64_t)key * a.dk.row, f.ak, a.scale, a.hd, lane);
+    write_row<T, DH>(a.dv.p + b * a.dv.batch + g * a.dv.head + (int64_t)key * a.dv.row, f.av, 1.f, a.hd, lane);
+  } else {
+    // [split][dk, dv][B][G][T][hd], fp32
+    const int64_t rows = (int64_t)a.B * a.G * a.T, r = ((int64_t)b * a.G + g) * a.T + key;
+    char *p0 = (char *)(a.part + ((int64_t)(2 * split) * rows + r) * a.hd);
+    char *p1 = (char *)(a.part + ((int64_t)(2 * split + 1) * rows + r) * a.hd);
+    write_row<float, DH>(p0, f.ak, a.scale, a.hd, lane);
+    write_row<float, DH>(p1, f.av, 1.f, a.hd, lane);
+  }
+}
+
+// dk and dv as the sums of their splits, in split order.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  const int64_t rows = (int64_t)a.B * a.G * a.T;
+  const int quads = a.hd / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= 2 * rows * quads) return;
+  const int64_t which = i / (rows * quads), r = i / quads % rows;
+  const int col = (int)(i % quads) * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < a.n_split; ++k) {
+    const float4 x = *reinterpret_cast<const float4 *>(a.part + ((2 * k + which) * rows + r) * a.hd + col);
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
+  }
+  const int64_t t = r % a.T, bg = r / a.T;
+  const AttnView &v = which ? a.dv : a.dk;
+  char *row = v.p + bg / a.G * v.batch + bg % a.G * v.head + t * v.row;
+  if constexpr (sizeof(T) == 2) {
+    bf16 w[4] = {(bf16)s.x, (bf16)s.y, (bf16)s.z, (bf16)s.w};
+    *reinterpret_cast<uint2 *>(row + col * 2) = __builtin_bit_cast(uint2, *(const u32x2 *)w);
+  } else {
+    *reinterpret_cast<float4 *>(row + col * 4) = s;
+  }
+}
+
+template <typename T, int DH, int BN>
+int launch(const AttnArgs &a, hipStream_t st) {
+  const int n = (a.T + 127) / 128;
+  attn_dq_kernel<T, DH, BN><<<dim3(n * a.H * a.B), dim3(256), 0, st>>>(a);
+  attn_dkv_kernel<T, DH, BN><<<dim3(n * a.G * a.n_split * a.B), dim3(256), 0, st>>>(a);
+  if (a.n_split > 1) {
+    const int64_t work = 2 * (int64_t)a.B * a.G * a.T * (a.hd / 4);
+    attn_join_kernel<T><<<dim3((unsigned)((work + 255) / 256)), dim3(256), 0, st>>>(a);
+  }
+  return DYNCONV_OK;
+}
+
+}  // namespace
+
+}  // namespace dynconv
