@@ -30,7 +30,7 @@ struct AttnArgs {
   float *delta;              // backward workspace: do . o, [B, H, T]
   float *part;               // backward workspace: dk / dv of the splits of a group (n_split > 1)
   int B, T, H, G, hd;
-  int n_split;  // dk/dv: blocks that share a key/value head's query heads
+  int n_split;  // dk/dv: blocks that share the queries of a tile of keys
   float scale;
   const int32_t *cu;
   int n_seqs;
@@ -81,6 +81,13 @@ __device__ __forceinline__ void doc_of(const int32_t *cu, int n_seqs, int T, int
   }
   start = min(max(cu[lo], 0), t);
   end = min(cu[lo + 1], T);
+}
+
+// The key from which on every row of a wave (queries qw .. qw+31, start: the lane's) sees
+// keys, so that tiles from there on to the diagonal need no mask.  Rows of no document are
+// let along: whatever they sum is not written.
+__device__ __forceinline__ int full_from(int start, int qw, int limit) {
+  return __builtin_amdgcn_readlane(start, __builtin_amdgcn_readfirstlane(min(31, max(0, limit - 1 - qw))));
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -239,19 +246,28 @@ __device__ __forceinline__ uint4 part_of(const uint4 &x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Whether rows r0 .. r0+31 of a tile hold an infinity or a NaN (uniform).
+// Whether rows r0 .. r0+31 of a tile hold an infinity or a NaN (uniform): the
+// largest bit pattern without its sign, two operations for a dword.
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 template <typename T, int DH>
 __device__ __forceinline__ bool not_finite(const unsigned char *t, int r0, int lane) {
   using TL = Tile<T, DH>;
-  uint32_t any = 0;
+  u16x2 top16 = {0, 0};
+  uint32_t top32 = 0;
 #pragma unroll
-  for (int s = 0; s < TL::PS; ++s)
+  for (int s = 0; s < TL::KS; ++s) {
+    const uint4 x = TL::rows(t, r0, s, lane);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int d = 0; d < TL::ND; ++d) {
-      const uint4 x = part_of<T, Part::ONE>(TL::cols(t, r0, s, d, lane));
-      any |= x.x | x.y | x.z | x.w;
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2)
+        top16 = __builtin_elementwise_max(top16, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+      else
+        top32 = max(top32, w[i] & 0x7fffffffu);
     }
-  return __ballot(any != 0) != 0;
+  }
+  const bool bad = sizeof(T) == 2 ? max(top16[0], top16[1]) >= 0x7f80u : top32 >= 0x7f800000u;
+  return __ballot(bad) != 0;
 }
 
 // acc += tile^T p over rows r0 .. r0+31 of which some hold an infinity or a NaN:
@@ -358,8 +374,7 @@ __device__ __forceinline__ void block_of(int n_heads_all, int &tile_rank, int &h
 int attn_fwd(const AttnArgs &a, int dtype, hipStream_t st);
 int attn_bwd(const AttnArgs &a, int dtype, hipStream_t st);
 int attn_bwd_fp32(const AttnArgs &a, hipStream_t st);
-// blocks that share a key/value head's query heads in the dk/dv kernel, and the
-// partial sums this takes (fp32 elements; 0 with one block)
+// blocks that share the (query head, query tile) pairs of a tile of keys in the dk/dv kernel
 int attn_bwd_splits(int64_t B, int64_t T, int H, int G);
 
 }  // namespace dynconv

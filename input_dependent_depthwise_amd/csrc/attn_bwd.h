@@ -67,15 +67,19 @@ struct Dq {
     return half_sum(sum);
   }
 
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int d = 0; d < TL::ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
+  }
+
   // All keys of the block; whether an infinity or a NaN in a masked tile was met (GUARD: never).
   template <bool GUARD>
   __device__ __forceinline__ bool pass(Lds &lds, int tid, int lane) {
     const int h = lane >> 5;
     bool met = false;
-#pragma unroll
-    for (int d = 0; d < TL::ND; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
+    clear();
     Stage<T, DH, BN, 256> sk, sv;
     int buf = 0;
     if (first <= last) {
@@ -156,7 +160,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
   doc_of(a.cu, a.n_seqs, a.T, f.last, tail, unused);
   tail = uniform(tail);
   f.w_first = uniform(f.start);  // (lane 0 has the lowest start)
-  f.w_full = __builtin_amdgcn_readlane(f.start, 31);
+  f.w_full = full_from(f.start, f.qw, f.limit);
 
   // a token of no document contributes nothing, whatever its rows hold
   const bool there = q < f.limit;
@@ -193,6 +197,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
 
   const bool met = f.template pass<false>(lds, tid, lane);
   if (__builtin_expect(__syncthreads_or(met), 0)) f.template pass<true>(lds, tid, lane);
+  if (!there) f.clear();
   if (q < a.T)
     write_row<T, DH>(a.dq.p + b * a.dq.batch + e * a.dq.head + (int64_t)q * a.dq.row, f.acc, a.scale, a.hd, lane);
 }
@@ -206,6 +211,7 @@ struct Dkv {
   };
   const AttnArgs &a;
   int b, e0, per;        // batch row, first query head, query heads
+  int split;             // which part of the (head, query tile) pairs, of a.n_split
   int k0, stop, limit;   // the block: its first key, the last query + 1 that sees any, valid tokens
   int kw, w_end;         // the wave: its first key; up to w_end every key is seen
   int key, end;          // the lane's key and its document's end
@@ -213,7 +219,7 @@ struct Dkv {
   uint4 kf[TL::KS], vf[TL::KS];
   f32x16 ak[TL::ND], av[TL::ND];
 
-  // All (head, query tile) pairs of the block, heads outside; returns as Dq::pass.
+  // The block's part of the (head, query tile) pairs, heads outside; returns as Dq::pass.
   template <bool GUARD>
   __device__ __forceinline__ bool pass(Lds &lds, int tid, int lane) {
     const int h = lane >> 5;
@@ -243,21 +249,24 @@ struct Dkv {
       sd.store(lds.tile[to][1], tid);
       if (tid < 2 * BN) lds.stat[to][tid / BN][tid % BN] = st;
     };
-    const int n_all = k0 < stop ? (stop - k0 + BN - 1) / BN * per : 0;
-    int buf = 0;
-    if (n_all > 0) {
-      fetch(e0, k0);
+    const int n_q = k0 < stop ? (stop - k0 + BN - 1) / BN : 0;
+    const int it0 = (int)((int64_t)n_q * per * split / a.n_split);
+    const int it1 = (int)((int64_t)n_q * per * (split + 1) / a.n_split);
+    int buf = 0, e = e0, qt = k0;
+    if (it0 < it1) {
+      e = e0 + it0 / n_q;
+      qt = k0 + it0 % n_q * BN;
+      fetch(e, qt);
       store(0);
     }
     __syncthreads();
-    int e = e0, qt = k0;
-    for (int it = 0; it < n_all; ++it) {
+    for (int it = it0; it < it1; ++it) {
       int e2 = e, qt2 = qt + BN;
       if (qt2 >= stop) {
         qt2 = k0;
         ++e2;
       }
-      const bool more = it + 1 < n_all;
+      const bool more = it + 1 < it1;
       if (more) fetch(e2, qt2);
       if (qt + BN > kw && kw < limit) {
         const unsigned char *ql = lds.tile[buf][0], *dl = lds.tile[buf][1];
@@ -322,8 +331,9 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a) {
   const int b = bg / (a.G * a.n_split), gs = bg % (a.G * a.n_split), g = gs / a.n_split, split = gs % a.n_split;
   F f{a};
   f.b = b;
-  f.per = group / a.n_split;
-  f.e0 = g * group + split * f.per;
+  f.per = group;
+  f.e0 = g * group;
+  f.split = split;
   f.k0 = rank * 128;
   f.c = a.scale * kLog2e;
   f.kw = f.k0 + wave * 32;

@@ -32,6 +32,13 @@ struct Fwd {
   f32x16 acc[TL::ND];
   float m, l;
 
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int d = 0; d < TL::ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
+  }
+
   // All keys of the block; whether an infinity or a NaN in a masked tile was met (GUARD: never).
   template <bool GUARD>
   __device__ __forceinline__ bool pass(Lds &lds, int tid, int lane) {
@@ -39,10 +46,7 @@ struct Fwd {
     bool met = false;
     m = -INFINITY;
     l = 0.f;
-#pragma unroll
-    for (int d = 0; d < TL::ND; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
+    clear();
     Stage<T, DH, BN, 256> sk, sv;
     int buf = 0;
     if (first <= last) {
@@ -156,7 +160,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
   f.first = uniform(f.first);
   f.last = min(q0 + 127, f.limit - 1);
   f.w_first = uniform(f.start);  // (lane 0 has the lowest start)
-  f.w_full = __builtin_amdgcn_readlane(f.start, 31);
+  f.w_full = full_from(f.start, f.qw, f.limit);
   const char *qrow = a.q.p + b * a.q.batch + e * a.q.head + (int64_t)q * a.q.row;
 #pragma unroll
   for (int s = 0; s < F::TL::KS; ++s) f.qf[s] = owned_chunk<T, DH>(qrow, q < a.T, 2 * s + h, a.hd);
@@ -166,10 +170,12 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
 
   const float l = half_sum(f.l);
   if (q < a.T) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const bool none = q >= f.limit || l == 0.f;  // no keys
+    if (none) f.clear();
+    const float inv = none ? 0.f : 1.f / l;
     write_row<T, DH>(a.o.p + b * a.o.batch + e * a.o.head + (int64_t)q * a.o.row, f.acc, inv, a.hd, lane);
     if (a.lse && h == 0)
-      a.lse[(int64_t)bh * a.T + q] = l == 0.f ? -INFINITY : f.m * a.scale + __builtin_amdgcn_logf(l) * kLn2;
+      a.lse[(int64_t)bh * a.T + q] = none ? -INFINITY : f.m * a.scale + __builtin_amdgcn_logf(l) * kLn2;
   }
 }
 
