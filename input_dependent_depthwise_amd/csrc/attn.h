@@ -116,29 +116,27 @@ __device__ __forceinline__ void mma_step(const uint4 &a, const uint4 &b, f32x16 
   }
 }
 
-// A tile of rows of DH elements in LDS, row-major, the 16-byte chunks of a row
-// permuted by an XOR that depends on the row: chunk j of row r lies at j ^
-// f(r).  f takes 16 consecutive rows to different banks for reads by rows (16
-// lanes, one chunk each), and 4 consecutive rows to different 64-byte groups
-// for the transposing reads (4 rows x 64 bytes for a half wave).
+// A tile of rows of DH elements in LDS, row-major with gaps: 64 bytes between the
+// rows of a group of four, 16 after the group.  Modulo the 256 bytes of the banks, the
+// rows of a group then start 64 bytes apart (a multiple of it), which the transposing reads need (4 rows
+// x 64 bytes for a half wave), and 16 consecutive rows in 16 different places, which
+// the reads by rows need (one 16-byte chunk each).  Gaps and not a permutation of the chunks: every read of
+// a tile is one lane address plus a constant (an XOR took 24 registers and as many adds a tile).
 template <typename T, int DH>
 struct Tile {
   static constexpr int E = 16 / (int)sizeof(T);  // elements of a chunk
   static constexpr int NC = DH / E;              // chunks of a row
-  static constexpr int ROW = DH * (int)sizeof(T);
+  static constexpr int ROW = DH * (int)sizeof(T) + 64, FOUR = 4 * ROW - 64 + 16;  // bytes from row to row, group to group
   static constexpr int KS = NC / 2;              // steps of a sum over DH
   static constexpr int PS = 32 / (2 * E);        // steps of a sum over 32 rows
   static constexpr int ND = DH / 32;
 
-  static __device__ __forceinline__ int swz(int r) {
-    if constexpr (NC == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-    return ((r & 3) << 2) | ((r >> 2) & 3);
-  }
-  static __device__ __forceinline__ int at(int r, int chunk) { return r * ROW + ((chunk ^ swz(r)) << 4); }
+  static constexpr int bytes(int rows) { return rows / 4 * FOUR; }
+  static __device__ __forceinline__ int at(int r, int chunk) { return (r >> 2) * FOUR + (r & 3) * ROW + (chunk << 4); }
 
   // rows r0 .. r0+31, step s of the sum over DH: lane l holds chunk 2s + l/32 of row l%32
   static __device__ __forceinline__ uint4 rows(const unsigned char *t, int r0, int s, int lane) {
-    return *reinterpret_cast<const uint4 *>(t + at(r0 + (lane & 31), 2 * s + (lane >> 5)));
+    return *reinterpret_cast<const uint4 *>(t + at(lane & 31, lane >> 5) + r0 / 4 * FOUR + s * 32);
   }
   // columns 32d .. 32d+31, step s of the sum over rows r0 .. r0+31, in the order in
   // which a score register block holds them: lane l, column l%32, half h = l/32:
@@ -146,21 +144,17 @@ struct Tile {
   static __device__ __forceinline__ uint4 cols(const unsigned char *t, int r0, int s, int d, int lane) {
     const int h = lane >> 5;
     if constexpr (sizeof(T) == 2) {
-      const int r = r0 + 16 * s + 4 * h + ((lane & 15) >> 2);
-      const int chunk = 4 * d + ((lane >> 3) & 2) + ((lane >> 1) & 1), b = (lane & 1) << 3;
-      const uint2 lo = read_tr16(t + at(r, chunk) + b), hi = read_tr16(t + at(r + 8, chunk) + b);
+      const unsigned char *p = t + at(4 * h + ((lane & 15) >> 2), ((lane >> 3) & 2) + ((lane >> 1) & 1)) + ((lane & 1) << 3) +
+                               (r0 / 4 + 4 * s) * FOUR + d * 64;
+      const uint2 lo = read_tr16(p), hi = read_tr16(p + 2 * FOUR);
       return make_uint4(lo.x, lo.y, hi.x, hi.y);
     } else {
-      const int r = r0 + 8 * s + 4 * h, chunk = 8 * d + ((lane & 31) >> 2), b = (lane & 3) << 2;
+      const unsigned char *p = t + at(4 * h, 0) + ((lane & 31) << 2) + (r0 / 4 + 2 * s) * FOUR + d * 128;
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t *>(t + at(r + i, chunk) + b);
+      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t *>(p + i * ROW);
       return make_uint4(w[0], w[1], w[2], w[3]);
     }
-  }
-  // one element
-  static __device__ __forceinline__ float elem(const unsigned char *t, int r, int col) {
-    return to_f32(*reinterpret_cast<const T *>(t + at(r, col / E) + (col % E) * (int)sizeof(T)));
   }
 };
 
@@ -200,11 +194,10 @@ struct Stage {
     }
   }
   __device__ __forceinline__ void store(unsigned char *t, int tid) const {
+    static_assert(THREADS / TL::NC % 4 == 0, "");
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int x = i * THREADS + tid;
-      *reinterpret_cast<uint4 *>(t + TL::at(x / TL::NC, x % TL::NC)) = r[i];
-    }
+    for (int i = 0; i < N; ++i)
+      *reinterpret_cast<uint4 *>(t + TL::at(tid / TL::NC, tid % TL::NC) + i * (THREADS / TL::NC / 4) * TL::FOUR) = r[i];
   }
 };
 
@@ -244,6 +237,14 @@ __device__ __forceinline__ uint4 part_of(const uint4 &x) {
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Marks loaded fragments as arrived.  Without it the wait for them stands at their first
+// use, inside the loop over tiles, where it waits for the next tile's loads as well.
+template <int N>
+__device__ __forceinline__ void arrived(uint4 (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(f[i].x), "+v"(f[i].y), "+v"(f[i].z), "+v"(f[i].w));
 }
 
 // Whether rows r0 .. r0+31 of a tile hold an infinity or a NaN (uniform): the

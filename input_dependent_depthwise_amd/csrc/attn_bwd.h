@@ -17,7 +17,7 @@ namespace {
 template <typename T, int DH, int BN>
 struct Dq {
   using TL = Tile<T, DH>;
-  typedef unsigned char Lds[2][2][BN * TL::ROW];  // [buffer][key, value]
+  typedef unsigned char Lds[2][2][TL::bytes(BN)];  // [buffer][key, value]
   // the block: keys of its head, their range, valid tokens
   const char *kh, *vh;
   int64_t krow, vrow;
@@ -74,10 +74,34 @@ struct Dq {
       for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
   }
 
+  // A block of 32 keys, from kt on, at rows 32 n of the tiles.
+  // (masked is no template argument: two copies of this body cost registers)
+  template <bool GUARD>
+  __device__ __forceinline__ void block(const unsigned char *kl, const unsigned char *vl, int n, int kt, bool masked,
+                                        bool &met, int lane) {
+    const int h = lane >> 5;
+    f32x16 p, dp;
+    scores(kl, vl, n, p, dp, lane);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -lse2)) * (dp[i] - delta);
+    if (masked) {
+      uint32_t seen = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int key = kt + score_row(i, h);
+        const bool see = key <= q && key >= start;
+        if (!see) p[i] = 0.f;
+        seen |= (uint32_t)see << i;
+      }
+      sum_rows_masked<GUARD, T, DH>(kl, 32 * n, p, seen, acc, met, lane);
+    }
+    if (!GUARD || !masked) sum_rows<T, DH>(kl, 32 * n, p, acc, lane);
+  }
+
   // All keys of the block; whether an infinity or a NaN in a masked tile was met (GUARD: never).
   template <bool GUARD>
   __device__ __forceinline__ bool pass(Lds &lds, int tid, int lane) {
-    const int h = lane >> 5;
     bool met = false;
     clear();
     Stage<T, DH, BN, 256> sk, sv;
@@ -89,40 +113,27 @@ struct Dq {
       sv.store(lds[0][1], tid);
     }
     __syncthreads();
+    // the next tile comes in halves, so that only one of them is held in registers at a time
     for (int kt = first; kt <= last; kt += BN) {
-      const bool more = kt + BN <= last;
-      if (more) {
-        sk.fetch(kh, krow, kt + BN, limit, hd, tid);
-        sv.fetch(vh, vrow, kt + BN, limit, hd, tid);
-      }
-      if (kt <= qw + 31 && kt + BN > w_first && qw < limit) {
-        const unsigned char *kl = lds[buf][0], *vl = lds[buf][1];
-        const bool masked = kt + BN - 1 > qw || kt < w_full;
-#pragma unroll
-        for (int n = 0; n < BN / 32; ++n) {
-          f32x16 p, dp;
-          scores(kl, vl, n, p, dp, lane);
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -lse2)) * (dp[i] - delta);
-          if (masked) {
-            uint32_t seen = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int key = kt + 32 * n + score_row(i, h);
-              const bool see = key <= q && key >= start;
-              if (!see) p[i] = 0.f;
-              seen |= (uint32_t)see << i;
-            }
-            sum_rows_masked<GUARD, T, DH>(kl, 32 * n, p, seen, acc, met, lane);
-          }
-          if (!GUARD || !masked) sum_rows<T, DH>(kl, 32 * n, p, acc, lane);
+      const bool more = kt + BN <= last, work = kt <= qw + 31 && kt + BN > w_first && qw < limit;
+      const unsigned char *kl = lds[buf][0], *vl = lds[buf][1];
+      const bool masked = kt + BN - 1 > qw || kt < w_full;
+      if (more) sk.fetch(kh, krow, kt + BN, limit, hd, tid);
+      if constexpr (GUARD || BN == 32) {
+#pragma unroll 1
+        for (int n = 0; n < BN / 32; ++n)
+          if (work) block<GUARD>(kl, vl, n, kt + 32 * n, masked, met, lane);
+        if (more) sv.fetch(vh, vrow, kt + BN, limit, hd, tid);
+        if (more) sk.store(lds[buf ^ 1][0], tid);
+      } else {
+        if (work) block<GUARD>(kl, vl, 0, kt, masked, met, lane);
+        if (more) {
+          sk.store(lds[buf ^ 1][0], tid);
+          sv.fetch(vh, vrow, kt + BN, limit, hd, tid);
         }
+        if (work) block<GUARD>(kl, vl, 1, kt + 32, masked, met, lane);
       }
-      if (more) {
-        sk.store(lds[buf ^ 1][0], tid);
-        sv.store(lds[buf ^ 1][1], tid);
-      }
+      if (more) sv.store(lds[buf ^ 1][1], tid);
       __syncthreads();
       buf ^= 1;
     }
@@ -178,6 +189,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < TL::E; ++i) f.delta = __builtin_fmaf(x[i], y[i], f.delta);
   }
+  arrived(f.qf);
+  arrived(f.df);
   f.delta = half_sum(f.delta);
   f.lse2 = INFINITY;  // log2 of the row's sum; +infinity: no key, every p is 0
   if (there) {
@@ -195,6 +208,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
   }
   if (q < a.T && h == 0) a.delta[(int64_t)bh * a.T + q] = f.delta;
 
+  asm volatile("" : "+v"(f.lse2));
   const bool met = f.template pass<false>(lds, tid, lane);
   if (__builtin_expect(__syncthreads_or(met), 0)) f.template pass<true>(lds, tid, lane);
   if (!there) f.clear();
@@ -206,7 +220,7 @@ template <typename T, int DH, int BN>
 struct Dkv {
   using TL = Tile<T, DH>;
   struct Lds {
-    unsigned char tile[2][2][BN * TL::ROW];  // [buffer][query, do]
+    unsigned char tile[2][2][TL::bytes(BN)];  // [buffer][query, do]
     float stat[2][2][BN];                    // log2 of each query's sum (+infinity: no key), its delta
   };
   const AttnArgs &a;
@@ -219,10 +233,50 @@ struct Dkv {
   uint4 kf[TL::KS], vf[TL::KS];
   f32x16 ak[TL::ND], av[TL::ND];
 
+  // A block of 32 queries, from qt on, at rows 32 n of the tiles.
+  template <bool GUARD>
+  __device__ __forceinline__ void block(const unsigned char *ql, const unsigned char *dl, const float (&stat)[2][BN],
+                                        int n, int qt, bool masked, bool &met, int lane) {
+    const int h = lane >> 5;
+    f32x16 p, dp;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = dp[i] = 0.f;
+#pragma unroll
+    for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(ql, 32 * n, s, lane), kf[s], p);
+#pragma unroll
+    for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(dl, 32 * n, s, lane), vf[s], dp);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 l4 = *reinterpret_cast<const float4 *>(&stat[0][32 * n + 8 * j + 4 * h]);
+      const float4 d4 = *reinterpret_cast<const float4 *>(&stat[1][32 * n + 8 * j + 4 * h]);
+      const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, de[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[4 * j + i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[4 * j + i], c, -ls[i]));
+        dp[4 * j + i] = p[4 * j + i] * (dp[4 * j + i] - de[i]);
+      }
+    }
+    if (masked) {
+      uint32_t seen = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int q = qt + score_row(i, h);
+        const bool see = q >= key && q < end;
+        if (!see) p[i] = dp[i] = 0.f;
+        seen |= (uint32_t)see << i;
+      }
+      sum_rows_masked<GUARD, T, DH>(dl, 32 * n, p, seen, av, met, lane);
+      sum_rows_masked<GUARD, T, DH>(ql, 32 * n, dp, seen, ak, met, lane);
+    }
+    if (!GUARD || !masked) {
+      sum_rows<T, DH>(dl, 32 * n, p, av, lane);
+      sum_rows<T, DH>(ql, 32 * n, dp, ak, lane);
+    }
+  }
+
   // The block's part of the (head, query tile) pairs, heads outside; returns as Dq::pass.
   template <bool GUARD>
   __device__ __forceinline__ bool pass(Lds &lds, int tid, int lane) {
-    const int h = lane >> 5;
     bool met = false;
 #pragma unroll
     for (int d = 0; d < TL::ND; ++d)
@@ -271,42 +325,12 @@ struct Dkv {
       if (qt + BN > kw && kw < limit) {
         const unsigned char *ql = lds.tile[buf][0], *dl = lds.tile[buf][1];
         const bool masked = qt < kw + 31 || qt + BN > w_end;
+        if constexpr (GUARD) {
+#pragma unroll 1
+          for (int n = 0; n < BN / 32; ++n) block<true>(ql, dl, lds.stat[buf], n, qt + 32 * n, masked, met, lane);
+        } else {
 #pragma unroll
-        for (int n = 0; n < BN / 32; ++n) {
-          f32x16 p, dp;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) p[i] = dp[i] = 0.f;
-#pragma unroll
-          for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(ql, 32 * n, s, lane), kf[s], p);
-#pragma unroll
-          for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(dl, 32 * n, s, lane), vf[s], dp);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 l4 = *reinterpret_cast<const float4 *>(&lds.stat[buf][0][32 * n + 8 * j + 4 * h]);
-            const float4 d4 = *reinterpret_cast<const float4 *>(&lds.stat[buf][1][32 * n + 8 * j + 4 * h]);
-            const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, de[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              p[4 * j + i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[4 * j + i], c, -ls[i]));
-              dp[4 * j + i] = p[4 * j + i] * (dp[4 * j + i] - de[i]);
-            }
-          }
-          if (masked) {
-            uint32_t seen = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int q = qt + 32 * n + score_row(i, h);
-              const bool see = q >= key && q < end;
-              if (!see) p[i] = dp[i] = 0.f;
-              seen |= (uint32_t)see << i;
-            }
-            sum_rows_masked<GUARD, T, DH>(dl, 32 * n, p, seen, av, met, lane);
-            sum_rows_masked<GUARD, T, DH>(ql, 32 * n, dp, seen, ak, met, lane);
-          }
-          if (!GUARD || !masked) {
-            sum_rows<T, DH>(dl, 32 * n, p, av, lane);
-            sum_rows<T, DH>(ql, 32 * n, dp, ak, lane);
-          }
+          for (int n = 0; n < BN / 32; ++n) block<false>(ql, dl, lds.stat[buf], n, qt + 32 * n, masked, met, lane);
         }
       }
       if (more) store(buf ^ 1);
@@ -320,7 +344,7 @@ struct Dkv {
 };
 
 template <typename T, int DH, int BN>
-__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(AttnArgs a) {
   using F = Dkv<T, DH, BN>;
   using TL = Tile<T, DH>;
   __shared__ __align__(16) typename F::Lds lds;
@@ -354,6 +378,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a) {
     f.kf[s] = owned_chunk<T, DH>(krow, there, 2 * s + h, a.hd);
     f.vf[s] = owned_chunk<T, DH>(vrow, there, 2 * s + h, a.hd);
   }
+  arrived(f.kf);
+  arrived(f.vf);
   const bool met = f.template pass<false>(lds, tid, lane);
   if (__builtin_expect(__syncthreads_or(met), 0)) f.template pass<true>(lds, tid, lane);
   if (key >= a.T) return;

@@ -19,7 +19,7 @@ constexpr float kSlack = 8.f;
 template <typename T, int DH, int BN>
 struct Fwd {
   using TL = Tile<T, DH>;
-  typedef unsigned char Lds[2][2][BN * TL::ROW];  // [buffer][key, value]
+  typedef unsigned char Lds[2][2][TL::bytes(BN)];  // [buffer][key, value]
   // the block: keys of its head, their range, valid tokens
   const char *kh, *vh;
   int64_t krow, vrow;
@@ -164,6 +164,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
   const char *qrow = a.q.p + b * a.q.batch + e * a.q.head + (int64_t)q * a.q.row;
 #pragma unroll
   for (int s = 0; s < F::TL::KS; ++s) f.qf[s] = owned_chunk<T, DH>(qrow, q < a.T, 2 * s + h, a.hd);
+
+  arrived(f.qf);
 
   const bool met = f.template pass<false>(lds, tid, lane);
   if (__builtin_expect(__syncthreads_or(met), 0)) f.template pass<true>(lds, tid, lane);
