@@ -239,6 +239,20 @@ __device__ __forceinline__ uint4 part_of(const uint4 &x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Asks the scheduler for a pipeline over the last N products: the LDS reads of AHEAD of
+// them first, then a product and the reads (READS each) of a later one in turn.  Left
+// alone it reads one fragment, waits for it and multiplies.
+template <int N, int READS, int MFMAS, int AHEAD>
+__device__ __forceinline__ void read_ahead() {
+  __builtin_amdgcn_sched_group_barrier(0x100, READS * AHEAD, 0);
+#pragma unroll
+  for (int i = 0; i < N - AHEAD; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, MFMAS, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, MFMAS * AHEAD, 0);
+}
+
 // Marks loaded fragments as arrived.  Without it the wait for them stands at their first
 // use, inside the loop over tiles, where it waits for the next tile's loads as well.
 template <int N>
@@ -318,6 +332,7 @@ __device__ __forceinline__ void sum_rows(const unsigned char *t, int r0, const f
 #pragma unroll
     for (int d = 0; d < TL::ND; ++d) mma_step<T>(TL::cols(t, r0, s, d, lane), b, acc[d]);
   }
+  if constexpr (sizeof(T) == 2) read_ahead<TL::PS * TL::ND, 2, 1, 4>();
 }
 
 // In a tile where some row is not seen by some owned row, a product with that pair's zero p would

@@ -38,6 +38,7 @@ struct Dq {
     for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(kl, 32 * n, s, lane), qf[s], p);
 #pragma unroll
     for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(vl, 32 * n, s, lane), df[s], dp);
+    if constexpr (sizeof(T) == 2) read_ahead<2 * TL::KS, 1, 1, 4>();
   }
 
   // delta = sum_j p (do . v_j) over the keys from the block's first query on.
@@ -245,6 +246,7 @@ struct Dkv {
     for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(ql, 32 * n, s, lane), kf[s], p);
 #pragma unroll
     for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(dl, 32 * n, s, lane), vf[s], dp);
+    if constexpr (sizeof(T) == 2) read_ahead<2 * TL::KS, 1, 1, 4>();
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float4 l4 = *reinterpret_cast<const float4 *>(&stat[0][32 * n + 8 * j + 4 * h]);

@@ -73,6 +73,7 @@ struct Fwd {
 #pragma unroll
           for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(kl, 32 * n, s, lane), qf[s], p[n]);
         }
+        if constexpr (sizeof(T) == 2) read_ahead<BN / 32 * TL::KS, 1, 1, 4>();
         uint32_t seen[BN / 32];
         if (masked) {
 #pragma unroll
