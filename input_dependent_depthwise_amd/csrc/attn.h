@@ -253,12 +253,33 @@ __device__ __forceinline__ void read_ahead() {
   __builtin_amdgcn_sched_group_barrier(0x008, MFMAS * AHEAD, 0);
 }
 
+// The same with VALU other vector operations after each product.
+template <int N, int READS, int AHEAD, int VALU>
+__device__ __forceinline__ void beside() {
+  __builtin_amdgcn_sched_group_barrier(0x100, READS * AHEAD, 0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (i < N - AHEAD) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    __builtin_amdgcn_sched_group_barrier(0x400, 1, 0);
+  }
+}
+
 // Marks loaded fragments as arrived.  Without it the wait for them stands at their first
 // use, inside the loop over tiles, where it waits for the next tile's loads as well.
 template <int N>
 __device__ __forceinline__ void arrived(uint4 (&f)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+v"(f[i].x), "+v"(f[i].y), "+v"(f[i].z), "+v"(f[i].w));
+}
+
+// The same for fragments that are to stay in accumulation registers, from which a product
+// takes an operand as well as from a vector register.
+template <int N>
+__device__ __forceinline__ void arrived_acc(uint4 (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+a"(f[i].x), "+a"(f[i].y), "+a"(f[i].z), "+a"(f[i].w));
 }
 
 // Whether rows r0 .. r0+31 of a tile hold an infinity or a NaN (uniform): the
@@ -332,7 +353,6 @@ __device__ __forceinline__ void sum_rows(const unsigned char *t, int r0, const f
 #pragma unroll
     for (int d = 0; d < TL::ND; ++d) mma_step<T>(TL::cols(t, r0, s, d, lane), b, acc[d]);
   }
-  if constexpr (sizeof(T) == 2) read_ahead<TL::PS * TL::ND, 2, 1, 4>();
 }
 
 // In a tile where some row is not seen by some owned row, a product with that pair's zero p would

@@ -97,7 +97,10 @@ struct Dq {
       }
       sum_rows_masked<GUARD, T, DH>(kl, 32 * n, p, seen, acc, met, lane);
     }
-    if (!GUARD || !masked) sum_rows<T, DH>(kl, 32 * n, p, acc, lane);
+    if (!GUARD || !masked) {
+      sum_rows<T, DH>(kl, 32 * n, p, acc, lane);
+      if constexpr (sizeof(T) == 2) read_ahead<TL::PS * TL::ND, 2, 1, 4>();
+    }
   }
 
   // All keys of the block; whether an infinity or a NaN in a masked tile was met (GUARD: never).
@@ -220,9 +223,10 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
 template <typename T, int DH, int BN>
 struct Dkv {
   using TL = Tile<T, DH>;
+  static_assert(BN <= 64, "");
   struct Lds {
     unsigned char tile[2][2][TL::bytes(BN)];  // [buffer][query, do]
-    float stat[2][2][BN];                    // log2 of each query's sum (+infinity: no key), its delta
+    float stat[2][2][BN];                    // lse log2 e (+infinity: no key) and delta of each query (FOLD: -lse / scale, -delta)
   };
   const AttnArgs &a;
   int b, e0, per;        // batch row, first query head, query heads
@@ -234,46 +238,159 @@ struct Dkv {
   uint4 kf[TL::KS], vf[TL::KS];
   f32x16 ak[TL::ND], av[TL::ND];
 
-  // A block of 32 queries, from qt on, at rows 32 n of the tiles.
-  template <bool GUARD>
-  __device__ __forceinline__ void block(const unsigned char *ql, const unsigned char *dl, const float (&stat)[2][BN],
-                                        int n, int qt, bool masked, bool &met, int lane) {
-    const int h = lane >> 5;
-    f32x16 p, dp;
+  // With bf16 the sums of the scores start at -lse / scale and those of do . v at -delta, read from
+  // LDS right into the accumulators, which saves their subtraction afterwards (fp32 sums
+  // would lose a digit to it).
+  static constexpr bool FOLD = sizeof(T) == 2;
+
+  // What the sums of the scores and of do . v of the 32 queries at rows 32 n start from.
+  __device__ __forceinline__ void begin(const float (&stat)[2][BN], int n, f32x16 &p, f32x16 &dp, int lane) const {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) p[i] = dp[i] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if constexpr (FOLD) {
+        x = *reinterpret_cast<const float4 *>(&stat[0][32 * n + 8 * j + 4 * (lane >> 5)]);
+        y = *reinterpret_cast<const float4 *>(&stat[1][32 * n + 8 * j + 4 * (lane >> 5)]);
+      }
+      p[4 * j] = x.x, p[4 * j + 1] = x.y, p[4 * j + 2] = x.z, p[4 * j + 3] = x.w;
+      dp[4 * j] = y.x, dp[4 * j + 1] = y.y, dp[4 * j + 2] = y.z, dp[4 * j + 3] = y.w;
+    }
+  }
+  // Probabilities in place of scores, ds in place of do . v, for four of them (register 4j on).
+  __device__ __forceinline__ void weights(const float (&stat)[2][BN], int n, int j, f32x16 &p, f32x16 &dp,
+                                          int lane) const {
+    float4 l4 = make_float4(0.f, 0.f, 0.f, 0.f), d4 = l4;
+    if constexpr (!FOLD) {
+      l4 = *reinterpret_cast<const float4 *>(&stat[0][32 * n + 8 * j + 4 * (lane >> 5)]);
+      d4 = *reinterpret_cast<const float4 *>(&stat[1][32 * n + 8 * j + 4 * (lane >> 5)]);
+    }
+    const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, de[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = 4 * j + i;
+      if constexpr (FOLD) {
+        p[k] = __builtin_amdgcn_exp2f(p[k] * c);
+        dp[k] *= p[k];
+      } else {
+        p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[k], c, -ls[i]));
+        dp[k] = p[k] * (dp[k] - de[i]);
+      }
+    }
+  }
+  // Which of the 32 queries from qt on see the lane's key; the others' scores to -infinity.
+  __device__ __forceinline__ uint32_t hide(int qt, f32x16 &p, int lane) const {
+    uint32_t seen = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int q = qt + score_row(i, lane >> 5);
+      const bool see = q >= key && q < end;
+      if (!see) p[i] = -INFINITY;
+      seen |= (uint32_t)see << i;
+    }
+    return seen;
+  }
+
+  // Zeros for what is not seen (its p is 0 already, unless its query's lse is a NaN, but do . v may
+  // have overflowed).
+  static __device__ __forceinline__ void drop(uint32_t seen, f32x16 &p, f32x16 &dp) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!(seen >> i & 1u)) p[i] = dp[i] = 0.f;
+  }
+
+  // The queries of one tile, from qt on.  Its products come in groups of four steps: scores and do . v
+  // of the first 32 queries, those of the next 32, the sums of the first, the sums of the
+  // next.  With one wave on a SIMD nobody else fills the gaps, so each group reads the operands of the
+  // one after it before its products, and the softmax of 32 queries runs beside the products of a later
+  // group; the scheduling barriers keep this order (left alone, every product waited for its own read).
+  __device__ __forceinline__ void tile(const unsigned char *ql, const unsigned char *dl, const float (&stat)[2][BN],
+                                       int qt, bool masked, bool &met, int lane) {
+    constexpr int NB = BN / 32, GA = TL::KS / 4, GC = TL::PS * TL::ND / 4;  // blocks; groups of a score, of a sum
+    constexpr int C0 = NB * 2 * GA, ALL = C0 + NB * 2 * GC;
+    f32x16 p[NB], dp[NB];
+    uint32_t seen[NB];
+    uint4 f[2][4];
+    auto read = [&](int g, uint4(&x)[4]) {
+      if (g < C0) {
+        const unsigned char *t = g / GA % 2 == 0 ? ql : dl;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = TL::rows(t, g / (2 * GA) * 32, g % GA * 4 + i, lane);
+      } else {
+        g -= C0;
+        const unsigned char *t = g / GC % 2 == 0 ? dl : ql;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = g % GC * 4 + i;
+          x[i] = TL::cols(t, g / (2 * GC) * 32, k / TL::ND, k % TL::ND, lane);
+        }
+      }
+    };
+    auto multiply = [&](int g, const uint4(&x)[4]) {
+      if (g < C0) {
+        const int n = g / (2 * GA), s = g % GA * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (g / GA % 2 == 0) mma_step<T>(x[i], kf[s + i], p[n]);
+          else mma_step<T>(x[i], vf[s + i], dp[n]);
+        }
+      } else {
+        g -= C0;
+        const int n = g / (2 * GC);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = g % GC * 4 + i;
+          if (g / GC % 2 == 0) mma_step<T>(x[i], score_frag<T>(p[n], k / TL::ND), av[k % TL::ND]);
+          else mma_step<T>(x[i], score_frag<T>(dp[n], k / TL::ND), ak[k % TL::ND]);
+        }
+      }
+    };
+    if (masked) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) met |= not_finite<T, DH>(dl, 32 * n, lane) || not_finite<T, DH>(ql, 32 * n, lane);
+    }
+    read(0, f[0]);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) begin(stat, n, p[n], dp[n], lane);
+#pragma unroll
+    for (int g = 0; g < ALL; ++g) {
+      // scores just finished are masked, weights just finished cleared
+      if (masked) {
+        if (g % (2 * GA) == 0 && g > 0 && g <= C0) seen[g / (2 * GA) - 1] = hide(qt + g / (2 * GA) * 32 - 32, p[g / (2 * GA) - 1], lane);
+        if (NB > 1 && g >= C0 && (g - C0) % (2 * GC) == 0) drop(seen[(g - C0) / (2 * GC)], p[(g - C0) / (2 * GC)], dp[(g - C0) / (2 * GC)]);
+      }
+      if (NB == 1 && g == C0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) weights(stat, 0, j, p[0], dp[0], lane);
+        if (masked) drop(seen[0], p[0], dp[0]);
+      }
+      if (g + 1 < ALL) read(g + 1, f[(g + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(g, f[g & 1]);
+      if (NB > 1) {
+        // the softmax of block n, spread over the groups from its scores to its sums
+        const int from = g < C0 ? 2 * GA : C0, many = g < C0 ? 2 * GA : 2 * GC, n = g < C0 ? 0 : 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (g >= from && g < from + many && j * many / 4 == g - from) weights(stat, n, j, p[n], dp[n], lane);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // The same for 32 queries, sums guarded where some query does not see some key.
+  __device__ __forceinline__ void guarded(const unsigned char *ql, const unsigned char *dl,
+                                          const float (&stat)[2][BN], int n, int qt, int lane) {
+    f32x16 p, dp;
+    begin(stat, n, p, dp, lane);
 #pragma unroll
     for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(ql, 32 * n, s, lane), kf[s], p);
 #pragma unroll
     for (int s = 0; s < TL::KS; ++s) mma_step<T>(TL::rows(dl, 32 * n, s, lane), vf[s], dp);
-    if constexpr (sizeof(T) == 2) read_ahead<2 * TL::KS, 1, 1, 4>();
+    const uint32_t seen = hide(qt, p, lane);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 l4 = *reinterpret_cast<const float4 *>(&stat[0][32 * n + 8 * j + 4 * h]);
-      const float4 d4 = *reinterpret_cast<const float4 *>(&stat[1][32 * n + 8 * j + 4 * h]);
-      const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, de[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[4 * j + i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[4 * j + i], c, -ls[i]));
-        dp[4 * j + i] = p[4 * j + i] * (dp[4 * j + i] - de[i]);
-      }
-    }
-    if (masked) {
-      uint32_t seen = 0;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int q = qt + score_row(i, h);
-        const bool see = q >= key && q < end;
-        if (!see) p[i] = dp[i] = 0.f;
-        seen |= (uint32_t)see << i;
-      }
-      sum_rows_masked<GUARD, T, DH>(dl, 32 * n, p, seen, av, met, lane);
-      sum_rows_masked<GUARD, T, DH>(ql, 32 * n, dp, seen, ak, met, lane);
-    }
-    if (!GUARD || !masked) {
-      sum_rows<T, DH>(dl, 32 * n, p, av, lane);
-      sum_rows<T, DH>(ql, 32 * n, dp, ak, lane);
-    }
+    for (int j = 0; j < 4; ++j) weights(stat, n, j, p, dp, lane);
+    drop(seen, p, dp);
+    sum_rows_guarded<T, DH>(dl, 32 * n, p, seen, av, lane);
+    sum_rows_guarded<T, DH>(ql, 32 * n, dp, seen, ak, lane);
   }
 
   // The block's part of the (head, query tile) pairs, heads outside; returns as Dq::pass.
@@ -294,10 +411,11 @@ struct Dkv {
         const int64_t at = ((int64_t)b * a.H + e) * a.T + i;
         if (which == 0) {
           const float v = i < limit ? a.lse[at] : -INFINITY;
-          st = v == -INFINITY ? INFINITY : v * kLog2e;
+          st = v == -INFINITY ? INFINITY : FOLD ? v / a.scale : v * kLog2e;
         } else {
           st = i < limit ? a.delta[at] : 0.f;
         }
+        if (FOLD) st = -st;
       }
     };
     auto store = [&](int to) {
@@ -326,13 +444,11 @@ struct Dkv {
       if (more) fetch(e2, qt2);
       if (qt + BN > kw && kw < limit) {
         const unsigned char *ql = lds.tile[buf][0], *dl = lds.tile[buf][1];
-        const bool masked = qt < kw + 31 || qt + BN > w_end;
         if constexpr (GUARD) {
 #pragma unroll 1
-          for (int n = 0; n < BN / 32; ++n) block<true>(ql, dl, lds.stat[buf], n, qt + 32 * n, masked, met, lane);
+          for (int n = 0; n < BN / 32; ++n) guarded(ql, dl, lds.stat[buf], n, qt + 32 * n, lane);
         } else {
-#pragma unroll
-          for (int n = 0; n < BN / 32; ++n) block<false>(ql, dl, lds.stat[buf], n, qt + 32 * n, masked, met, lane);
+          tile(ql, dl, lds.stat[buf], qt, qt < kw + 31 || qt + BN > w_end, met, lane);
         }
       }
       if (more) store(buf ^ 1);
@@ -380,8 +496,13 @@ __global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 2 : 1) void attn_
     f.kf[s] = owned_chunk<T, DH>(krow, there, 2 * s + h, a.hd);
     f.vf[s] = owned_chunk<T, DH>(vrow, there, 2 * s + h, a.hd);
   }
-  arrived(f.kf);
-  arrived(f.vf);
+  if constexpr (DH == 128) {
+    arrived_acc(f.kf);
+    arrived_acc(f.vf);
+  } else {
+    arrived(f.kf);
+    arrived(f.vf);
+  }
   const bool met = f.template pass<false>(lds, tid, lane);
   if (__builtin_expect(__syncthreads_or(met), 0)) f.template pass<true>(lds, tid, lane);
   if (key >= a.T) return;

@@ -120,7 +120,10 @@ struct Fwd {
         }
         if (!GUARD || !masked) {
 #pragma unroll
-          for (int n = 0; n < BN / 32; ++n) sum_rows<T, DH>(vl, 32 * n, p[n], acc, lane);
+          for (int n = 0; n < BN / 32; ++n) {
+            sum_rows<T, DH>(vl, 32 * n, p[n], acc, lane);
+            if constexpr (sizeof(T) == 2) read_ahead<TL::PS * TL::ND, 2, 1, 4>();
+          }
         }
       }
       if (more) {
