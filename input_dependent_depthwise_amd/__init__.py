@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -112,7 +113,7 @@ def lib() -> ctypes.CDLL:
         L.dynconv_abi_version.restype = ctypes.c_int
         L.dynconv_trace_next.argtypes = [ctypes.c_int, P, P]
         L.dynconv_trace_next.restype = ctypes.c_int
-        PA, PR, PV = ctypes.POINTER(Attn), ctypes.POINTER(Rotary), ctypes.POINTER(View)
+        PA = PR = PV = P  # Attn, Rotary and View, by reference or as packed bytes
         D, SZ, I64 = ctypes.c_double, ctypes.c_size_t, ctypes.c_int64
         L.dynconv_rope_freqs.argtypes = [ctypes.c_int, D, D, D, D, D, P]
         L.dynconv_rope.argtypes = [PA, PR, PV, P, PV, P]
@@ -346,51 +347,69 @@ class DynConvFn(torch.autograd.Function):
 
 
 # --- the Q/K/V path behind the convolution ------------------------------------------------------
+#
+# These calls are made once a token and layer in serving, so what they cost on the host
+# counts: the structs are packed directly (as View, Attn and Rotary lay them out) and the
+# raw stream is asked for, 12 us a rotary call -> 8.
+
+_VIEW, _ATTN, _ROTARY = struct.Struct("Pqqq").pack, struct.Struct("qqiiiifiPq").pack, struct.Struct("iiifP").pack
 
 
-def _view(t: torch.Tensor, what: str, heads: int | None = None, like=None, dtype=None) -> View:
-    """View struct of a [B, T, heads, head_dim] tensor whose last axis is contiguous."""
-    if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
-        raise ValueError(f"{what}: expected [B, T, heads, head_dim] with a contiguous last axis, got "
-                         f"{tuple(t.shape)} strides {t.stride()}")
-    if like is not None and (t.shape[0], t.shape[1], t.shape[3]) != like:
-        raise ValueError(f"{what}: sizes {tuple(t.shape)} do not fit [B, T, head_dim] = {like}")
-    if heads is not None and t.shape[2] != heads:
-        raise ValueError(f"{what}: {t.shape[2]} heads where {heads} were expected")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{what}: {t.dtype} where {dtype} was expected")
-    if not t.is_cuda:
-        raise TypeError(f"{what} must be on the GPU")
+def _pack_view(t: torch.Tensor, what: str, shape, dtype) -> bytes:
+    """The View of a [B, T, heads, head_dim] (or [B, heads, head_dim]) tensor of the given shape and dtype."""
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{what}: expected a {dtype} tensor on the GPU, got {t.dtype} on {t.device}")
     s = t.stride()
-    return View(t.data_ptr(), s[0], s[1], s[2])
+    if s[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{what}: the last axis must be contiguous, got strides {s}")
+    return _VIEW(t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else _VIEW(t.data_ptr(), s[0], 0, s[1])
 
 
-def _int32(t, what: str, shape: tuple | None = None):
+def _dims(t: torch.Tensor, what: str, n: int):
+    if t.dim() != n:
+        raise ValueError(f"{what}: expected {n} axes, got the shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _int32(t, what: str, shape=None) -> int:
+    """Address of a contiguous int32 tensor on the GPU, 0 for None."""
     if t is None:
-        return None
-    if t.dtype != torch.int32 or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
-        raise TypeError(f"{what} must be a contiguous int32 tensor" + (f" of shape {shape}" if shape else ""))
-    if not t.is_cuda:
-        raise TypeError(f"{what} must be on the GPU")
+        return 0
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise TypeError(f"{what} must be a contiguous int32 tensor on the GPU"
+                        + (f" of shape {tuple(shape)}" if shape is not None else ""))
     return t.data_ptr()
 
 
-def _attn(q: torch.Tensor, n_kv_heads: int, scale, cu_seqlens) -> Attn:
-    B, T, H, hd = q.shape
+def _pack_attn(B, T, H, G, hd, dtype, scale, cu_seqlens) -> bytes:
     if cu_seqlens is None:
-        return Attn(B, T, H, n_kv_heads, hd, _dtype_code(q.dtype), scale or 0.0, 0, None, 0)
+        return _ATTN(B, T, H, G, hd, _dtype_code(dtype), scale or 0.0, 0, 0, 0)
     if cu_seqlens.dim() != 1:
         raise TypeError("cu_seqlens must be a contiguous 1-d int32 tensor")
-    return Attn(B, T, H, n_kv_heads, hd, _dtype_code(q.dtype), scale or 0.0, 0, _int32(cu_seqlens, "cu_seqlens"),
-                cu_seqlens.numel() - 1)
+    return _ATTN(B, T, H, G, hd, _dtype_code(dtype), scale or 0.0, 0, _int32(cu_seqlens, "cu_seqlens"),
+                 cu_seqlens.shape[0] - 1)
 
 
-def _rotary(freqs: torch.Tensor, interleaved: bool, inverse: bool, factor: float) -> Rotary:
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise TypeError("freqs must be a contiguous 1-d float64 tensor (radians per position, one per pair)")
-    if not freqs.is_cuda:
-        raise TypeError("freqs must be on the GPU")
-    return Rotary(2 * freqs.numel(), int(interleaved), int(inverse), factor, freqs.data_ptr())
+def _pack_rotary(freqs: torch.Tensor, interleaved, inverse, factor) -> bytes:
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous() or not freqs.is_cuda:
+        raise TypeError("freqs must be a contiguous 1-d float64 tensor on the GPU (radians per position, one per pair)")
+    return _ROTARY(2 * freqs.shape[0], 1 if interleaved else 0, 1 if inverse else 0, factor, freqs.data_ptr())
+
+
+def _raw_stream(t: torch.Tensor, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
+
+
+def _lse(lse, shape) -> int:
+    if lse.dtype != torch.float32 or lse.shape != shape or not lse.is_contiguous() or not lse.is_cuda:
+        raise TypeError(f"lse must be a contiguous float32 tensor {list(shape)} on the GPU")
+    return lse.data_ptr()
+
+
+def _new(like: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def dynconv_rope_freqs(rot_dim: int, base: float = 10000.0, *, stretch: float = 1.0, trained_len: float = 0.0,
@@ -409,18 +428,20 @@ def dynconv_rope_freqs(rot_dim: int, base: float = 10000.0, *, stretch: float = 
 
 def dynconv_rope(x, freqs, *, positions=None, cu_seqlens=None, interleaved=False, factor=1.0, inverse=False, out=None,
                  stream=None):
-    """Rotary positions: x [B, T, heads, head_dim] (any strides) with its first
-    2 * len(freqs) elements turned, as a new tensor or into ``out`` (x itself:
-    in place).  positions: int32 [B, T], or the token's index in its row or,
-    with cu_seqlens, in its document.  inverse: the backward."""
-    a = _attn(x, 1, None, cu_seqlens)
-    r = _rotary(freqs, interleaved, inverse, factor)
+    """Rotary positions: x [B, T, heads, head_dim] (any strides with a contiguous
+    last axis) with its first 2 * len(freqs) elements turned, as a new tensor or
+    into ``out`` (x itself: in place).  positions: int32 [B, T], or the token's
+    index in its row or, with cu_seqlens, in its document.  inverse: the backward."""
+    B, T, H, hd = shape = _dims(x, "x", 4)
+    dt = x.dtype
+    a = _pack_attn(B, T, H, 1, hd, dt, None, cu_seqlens)
+    r = _pack_rotary(freqs, interleaved, inverse, factor)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    vx = _view(x, "x")
-    vy = _view(out, "out", x.shape[2], (x.shape[0], x.shape[1], x.shape[3]), x.dtype)
-    rc = lib().dynconv_rope(a, r, vx, _int32(positions, "positions", tuple(x.shape[:2])), vy, _stream(stream))
-    _check(rc, "dynconv_rope")
+        out = _new(x)
+    rc = lib().dynconv_rope(a, r, _pack_view(x, "x", shape, dt), _int32(positions, "positions", (B, T)),
+                            _pack_view(out, "out", shape, dt), _raw_stream(x, stream))
+    if rc:
+        _check(rc, "dynconv_rope")
     return out
 
 
@@ -429,47 +450,42 @@ def dynconv_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, o=None, lse=None, 
     v [B, T, n_kv_heads, head_dim] (any strides with a contiguous last axis).
     Returns o (and lse, fp32 [B, n_heads, T], when want_lse).  scale: default
     1 / sqrt(head_dim).  cu_seqlens: packed documents (B must be 1)."""
-    G, dt = k.shape[2], q.dtype
-    a = _attn(q, G, scale, cu_seqlens)
-    like = (a.B, a.T, a.head_dim)
+    B, T, H, hd = shape = _dims(q, "q", 4)
+    G, dt = _dims(k, "k", 4)[2], q.dtype
+    kv = (B, T, G, hd)
     if o is None:
-        o = torch.empty(q.shape, dtype=dt, device=q.device)
+        o = _new(q)
     if lse is None and want_lse:
-        lse = torch.empty((a.B, a.n_heads, a.T), dtype=torch.float32, device=q.device)
-    rc = lib().dynconv_attn_fwd(a, _view(q, "q"), _view(k, "k", G, like, dt), _view(v, "v", G, like, dt),
-                                _view(o, "o", a.n_heads, like, dt), _lse(lse, a), _stream(stream))
-    _check(rc, "dynconv_attn_fwd")
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+    rc = lib().dynconv_attn_fwd(_pack_attn(B, T, H, G, hd, dt, scale, cu_seqlens), _pack_view(q, "q", shape, dt),
+                                _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt), _pack_view(o, "o", shape, dt),
+                                None if lse is None else _lse(lse, (B, H, T)), _raw_stream(q, stream))
+    if rc:
+        _check(rc, "dynconv_attn_fwd")
     return (o, lse) if want_lse else o
-
-
-def _lse(lse, a: Attn):
-    if lse is None:
-        return None
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (a.B, a.n_heads, a.T) or not lse.is_contiguous():
-        raise TypeError(f"lse must be a contiguous float32 tensor [{a.B}, {a.n_heads}, {a.T}]")
-    if not lse.is_cuda:
-        raise TypeError("lse must be on the GPU")
-    return lse.data_ptr()
 
 
 def dynconv_attn_bwd(q, k, v, o, lse, d_o, *, scale=None, cu_seqlens=None, out=None, workspace=None, stream=None):
     """Backward of dynconv_attn_fwd from its inputs, o, lse and d_o.  Returns
     dict(dq, dk, dv); ``out`` may hold any of them (views of one gradient row,
     for instance)."""
-    G, dt = k.shape[2], q.dtype
-    a = _attn(q, G, scale, cu_seqlens)
-    like, H = (a.B, a.T, a.head_dim), a.n_heads
+    B, T, H, hd = shape = _dims(q, "q", 4)
+    G, dt = _dims(k, "k", 4)[2], q.dtype
+    kv = (B, T, G, hd)
+    a = _pack_attn(B, T, H, G, hd, dt, scale, cu_seqlens)
     g = dict(out or {})
     for name, t in (("dq", q), ("dk", k), ("dv", v)):
         if name not in g:
-            g[name] = torch.empty(t.shape, dtype=dt, device=q.device)
-    ws = _workspace(int(lib().dynconv_attn_bwd_workspace_bytes(a)), q.device, workspace)
-    rc = lib().dynconv_attn_bwd(
-        a, _view(q, "q"), _view(k, "k", G, like, dt), _view(v, "v", G, like, dt), _view(o, "o", H, like, dt),
-        _lse(lse, a), _view(d_o, "d_o", H, like, dt), _view(g["dq"], "dq", H, like, dt),
-        _view(g["dk"], "dk", G, like, dt), _view(g["dv"], "dv", G, like, dt), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream))
-    _check(rc, "dynconv_attn_bwd")
+            g[name] = _new(t)
+    L = lib()
+    ws = _workspace(L.dynconv_attn_bwd_workspace_bytes(a), q.device, workspace)
+    rc = L.dynconv_attn_bwd(
+        a, _pack_view(q, "q", shape, dt), _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt),
+        _pack_view(o, "o", shape, dt), _lse(lse, (B, H, T)), _pack_view(d_o, "d_o", shape, dt),
+        _pack_view(g["dq"], "dq", shape, dt), _pack_view(g["dk"], "dk", kv, dt), _pack_view(g["dv"], "dv", kv, dt),
+        ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(q, stream))
+    if rc:
+        _check(rc, "dynconv_attn_bwd")
     return g
 
 
@@ -481,19 +497,20 @@ def dynconv_attn_decode(q, k, v, k_cache, v_cache, lengths, *, scale=None, freqs
     rotary plan (freqs None: not), k and v stored in the caches' rows lengths[b],
     and o [B, n_heads, head_dim] returned.  A slot with lengths[b] < 0 (or a full
     one) is idle: its o is zero."""
-    q4, k4, v4 = q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1)
-    G, dt, cap = k.shape[1], q.dtype, k_cache.shape[1]
-    a = _attn(q4, G, scale, None)
-    like, rows = (a.B, 1, a.head_dim), (a.B, cap, a.head_dim)
+    B, H, hd = shape = _dims(q, "q", 3)
+    G, dt, cap = _dims(k, "k", 3)[1], q.dtype, _dims(k_cache, "k_cache", 4)[1]
+    kv, rows = (B, G, hd), (B, cap, G, hd)
+    a = _pack_attn(B, 1, H, G, hd, dt, scale, None)
     if o is None:
-        o = torch.empty(q.shape, dtype=dt, device=q.device)
-    r = None if freqs is None else _rotary(freqs, interleaved, False, factor)
-    nbytes = int(lib().dynconv_attn_decode_workspace_bytes(a, cap))
+        o = _new(q)
+    L = lib()
+    nbytes = L.dynconv_attn_decode_workspace_bytes(a, cap)
     ws = _workspace(nbytes, q.device, workspace) if nbytes else None
-    rc = lib().dynconv_attn_decode(
-        a, r, _view(q4, "q"), _view(k4, "k", G, like, dt), _view(v4, "v", G, like, dt),
-        _view(k_cache, "k_cache", G, rows, dt), _view(v_cache, "v_cache", G, rows, dt), cap,
-        _int32(lengths, "lengths", (a.B,)), _view(o.unsqueeze(1), "o", a.n_heads, like, dt), _ptr(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
-    _check(rc, "dynconv_attn_decode")
+    rc = L.dynconv_attn_decode(
+        a, None if freqs is None else _pack_rotary(freqs, interleaved, False, factor), _pack_view(q, "q", shape, dt),
+        _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt), _pack_view(k_cache, "k_cache", rows, dt),
+        _pack_view(v_cache, "v_cache", rows, dt), cap, _int32(lengths, "lengths", (B,)), _pack_view(o, "o", shape, dt),
+        _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(q, stream))
+    if rc:
+        _check(rc, "dynconv_attn_decode")
     return o
