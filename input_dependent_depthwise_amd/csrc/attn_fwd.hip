@@ -196,6 +196,7 @@ int launch(const AttnArgs &a, hipStream_t st) {
 
 int attn_fwd(const AttnArgs &a, int dtype, hipStream_t st) {
   if (dtype == DYNCONV_BF16) return a.hd <= 64 ? launch<bf16, 64, 64>(a, st) : launch<bf16, 128, 64>(a, st);
+  if (a.hd <= 32) return launch<float, 32, 64>(a, st);
   return a.hd <= 64 ? launch<float, 64, 32>(a, st) : launch<float, 128, 32>(a, st);
 }
 
