@@ -514,3 +514,40 @@ def dynconv_attn_decode(q, k, v, k_cache, v_cache, lengths, *, scale=None, freqs
     if rc:
         _check(rc, "dynconv_attn_decode")
     return o
+
+
+class QKVAttnFn(torch.autograd.Function):
+    """autograd wrapper of what follows the convolution on the Q/K/V path:
+    o = QKVAttnFn.apply(row, n_heads, n_kv_heads, freqs[, interleaved, factor, scale, cu_seqlens]).
+
+    row [B, T, (n_heads + 2 n_kv_heads) head_dim] (query, key and value heads
+    side by side, as DynConvFn returns it) -> rotary positions on its query and
+    key heads (freqs None: none) -> causal attention -> o [B, T, n_heads, head_dim].
+    The backward writes one gradient row, turned back in place.
+    """
+
+    @staticmethod
+    def forward(ctx, row, n_heads, n_kv_heads, freqs, interleaved=False, factor=1.0, scale=None, cu_seqlens=None):
+        H, G = n_heads, n_kv_heads
+        heads = row.view(row.shape[0], row.shape[1], H + 2 * G, -1)
+        qk, v = heads[:, :, :H + G], heads[:, :, H + G:]
+        if freqs is not None:
+            qk = dynconv_rope(qk, freqs, cu_seqlens=cu_seqlens, interleaved=interleaved, factor=factor)
+        o, lse = dynconv_attn_fwd(qk[:, :, :H], qk[:, :, H:], v, scale=scale, cu_seqlens=cu_seqlens, want_lse=True)
+        ctx.save_for_backward(qk, v, o, lse, freqs, cu_seqlens)
+        ctx.args = H, interleaved, factor, scale
+        return o
+
+    @staticmethod
+    def backward(ctx, d_o):
+        qk, v, o, lse, freqs, cu_seqlens = ctx.saved_tensors
+        H, interleaved, factor, scale = ctx.args
+        both = qk.shape[2]
+        B, T, heads, hd = qk.shape[0], qk.shape[1], both + v.shape[2], qk.shape[3]
+        row = torch.empty((B, T, heads, hd), dtype=qk.dtype, device=qk.device)
+        dynconv_attn_bwd(qk[:, :, :H], qk[:, :, H:], v, o, lse, d_o.contiguous(), scale=scale, cu_seqlens=cu_seqlens,
+                         out={"dq": row[:, :, :H], "dk": row[:, :, H:both], "dv": row[:, :, both:]})
+        if freqs is not None:
+            dynconv_rope(row[:, :, :both], freqs, cu_seqlens=cu_seqlens, interleaved=interleaved, factor=factor,
+                         inverse=True, out=row[:, :, :both])
+        return (row.view(B, T, heads * hd),) + (None,) * 7
