@@ -176,22 +176,25 @@ __device__ __forceinline__ uint4 score_frag(const f32x16 &p, int s) {
 __device__ __forceinline__ int score_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 
 // Copies rows [row0, row0 + ROWS) of one head into a tile, through registers:
-// fetch() issues the loads, store() writes what came.  Rows at or past `limit`
-// and elements past head_dim come as zeros.
+// fetch() issues the loads, store() writes what came.  Rows at or past `limit` (> row0)
+// and elements past head_dim come as zeros (of rows that overlap each other in
+// memory, rows past `limit` come as whatever rows before it hold; nothing depends on them):
+// the buffer ends with row limit - 1, so a load is one address sum.
 template <typename T, int DH, int ROWS, int THREADS>
 struct Stage {
   using TL = Tile<T, DH>;
   static constexpr int N = ROWS * TL::NC / THREADS;
-  static_assert(ROWS * TL::NC % THREADS == 0, "");
+  static_assert(ROWS * TL::NC % THREADS == 0 && THREADS % TL::NC == 0, "");
   uint4 r[N];
   __device__ __forceinline__ void fetch(const char *head, int64_t row_bytes, int row0, int limit, int hd, int tid) {
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(head + (int64_t)row0 * row_bytes, kOutside);
+    const int64_t bytes = (int64_t)(limit - row0 - 1) * row_bytes + hd * (int)sizeof(T);
+    const __amdgpu_buffer_rsrc_t rs =
+        make_rsrc(head + (int64_t)row0 * row_bytes, (uint32_t)(bytes < (int64_t)kOutside ? bytes : (int64_t)kOutside));
+    const int chunk = tid % TL::NC;
+    const uint32_t at = chunk * TL::E < hd ? (uint32_t)(tid / TL::NC) * (uint32_t)row_bytes + chunk * 16u : kOutside;
+    const uint32_t step = (uint32_t)(THREADS / TL::NC) * (uint32_t)row_bytes;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int x = i * THREADS + tid, row = x / TL::NC, chunk = x % TL::NC;
-      const bool in = row0 + row < limit && chunk * TL::E < hd;
-      r[i] = buf_load16(rs, in ? (uint32_t)row * (uint32_t)row_bytes + chunk * 16u : kOutside);
-    }
+    for (int i = 0; i < N; ++i) r[i] = buf_load16(rs, at + i * step);
   }
   __device__ __forceinline__ void store(unsigned char *t, int tid) const {
     static_assert(THREADS / TL::NC % 4 == 0, "");
