@@ -146,7 +146,7 @@ struct Dq {
 };
 
 template <typename T, int DH, int BN>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 3 : 2) void attn_dq_kernel(AttnArgs a) {
   using F = Dq<T, DH, BN>;
   using TL = Tile<T, DH>;
   __shared__ __align__(16) typename F::Lds lds;

@@ -138,7 +138,7 @@ struct Fwd {
 };
 
 template <typename T, int DH, int BN>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 3 : 2) void attn_fwd_kernel(AttnArgs a) {
   using F = Fwd<T, DH, BN>;
   __shared__ __align__(16) typename F::Lds lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
