@@ -197,7 +197,7 @@ struct Stage {
     for (int i = 0; i < N; ++i) r[i] = buf_load16(rs, at + i * step);
   }
   __device__ __forceinline__ void store(unsigned char *t, int tid) const {
-    static_assert(THREADS / TL::NC % 4 == 0, "");
+    static_assert(THREADS / TL::NC % 4 == 0, "");  // (whole groups of rows, so that a constant takes one to the next)
 #pragma unroll
     for (int i = 0; i < N; ++i)
       *reinterpret_cast<uint4 *>(t + TL::at(tid / TL::NC, tid % TL::NC) + i * (THREADS / TL::NC / 4) * TL::FOUR) = r[i];
@@ -374,25 +374,49 @@ __device__ __forceinline__ void sum_rows_masked(const unsigned char *t, int r0, 
   }
 }
 
-// Writes an accumulator block acc[column][owned row] times f as a row of T.
+// Writes 32 columns (from 32 d on) of an accumulator block times f into a row of T.
+template <typename T>
+__device__ __forceinline__ void write_part(char *row, const f32x16 &acc, int d, float f, int hd, int lane) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int col = 32 * d + 8 * b + 4 * (lane >> 5);
+    if (col >= hd) continue;
+    if constexpr (sizeof(T) == 2) {
+      bf16 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = (bf16)(acc[4 * b + i] * f);
+      *reinterpret_cast<uint2 *>(row + col * 2) = __builtin_bit_cast(uint2, *(const u32x2 *)w);
+    } else {
+      *reinterpret_cast<float4 *>(row + col * 4) =
+          make_float4(acc[4 * b] * f, acc[4 * b + 1] * f, acc[4 * b + 2] * f, acc[4 * b + 3] * f);
+    }
+  }
+}
 template <typename T, int DH>
 __device__ __forceinline__ void write_row(char *row, const f32x16 (&acc)[DH / 32], float f, int hd, int lane) {
 #pragma unroll
-  for (int d = 0; d < DH / 32; ++d)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int col = 32 * d + 8 * b + 4 * (lane >> 5);
-      if (col >= hd) continue;
-      if constexpr (sizeof(T) == 2) {
-        bf16 w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = (bf16)(acc[d][4 * b + i] * f);
-        *reinterpret_cast<uint2 *>(row + col * 2) = __builtin_bit_cast(uint2, *(const u32x2 *)w);
-      } else {
-        *reinterpret_cast<float4 *>(row + col * 4) =
-            make_float4(acc[d][4 * b] * f, acc[d][4 * b + 1] * f, acc[d][4 * b + 2] * f, acc[d][4 * b + 3] * f);
-      }
-    }
+  for (int d = 0; d < DH / 32; ++d) write_part<T>(row, acc[d], d, f, hd, lane);
+}
+
+// With fewer than one block of 128 queries for a CU, the chip waits for the longest chain of
+// keys.  The forward and dq then take blocks of 32 queries whose 4 waves share the keys, every
+// fourth tile of 32 each in LDS of its own, and join their sums at the end: four times the
+// blocks, a quarter of the chain.
+constexpr int kFewBlocks = 256;
+inline bool few_blocks(const AttnArgs &a) { return (int64_t)((a.T + 127) / 128) * a.H * a.B < kFewBlocks; }
+
+template <typename T, int DH>
+struct FewLds {
+  union {
+    unsigned char tile[4][2][Tile<T, DH>::bytes(32)];  // [wave][key, value]
+    float sum[4][DH / 2][64];                          // [wave][accumulator register][lane]
+  };
+  float top[4][32], tot[4][32];
+};
+// A wave's own LDS written before it is read (by other lanes).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // Blocks over (tile, head, batch row): the tiles with most work first, and,

@@ -103,6 +103,59 @@ struct Dq {
     }
   }
 
+  // As delta_of_block, one tile of 32 keys from kt on (a wave's share).
+  __device__ __forceinline__ float delta_of_tile(unsigned char (&mine)[2][TL::bytes(32)], int kt, int lane) const {
+    const int h = lane >> 5;
+    Stage<T, DH, 32, 64> sk, sv;
+    sk.fetch(kh, krow, kt, limit, hd, lane);
+    sv.fetch(vh, vrow, kt, limit, hd, lane);
+    sk.store(mine[0], lane);
+    sv.store(mine[1], lane);
+    wave_sync();
+    f32x16 p, dp;
+    scores(mine[0], mine[1], 0, p, dp, lane);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int key = kt + score_row(i, h);
+      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -lse2)) * dp[i];
+      if (key <= q && key >= start) sum += x;
+    }
+    wave_sync();
+    return half_sum(sum);
+  }
+
+  // Every fourth tile of the block's keys, for one of its four waves; returns as pass().
+  template <bool GUARD>
+  __device__ __forceinline__ bool pass_few(unsigned char (&mine)[2][TL::bytes(32)], int wave, int lane) {
+    static_assert(BN == 32, "");
+    bool met = false;
+    clear();
+    Stage<T, DH, 32, 64> sk, sv;
+    int kt = first + 32 * wave;
+    if (kt <= last) {
+      sk.fetch(kh, krow, kt, limit, hd, lane);
+      sv.fetch(vh, vrow, kt, limit, hd, lane);
+      sk.store(mine[0], lane);
+      sv.store(mine[1], lane);
+    }
+    for (; kt <= last; kt += 128) {
+      const bool more = kt + 128 <= last;
+      wave_sync();
+      if (more) {
+        sk.fetch(kh, krow, kt + 128, limit, hd, lane);
+        sv.fetch(vh, vrow, kt + 128, limit, hd, lane);
+      }
+      block<GUARD>(mine[0], mine[1], 0, kt, kt + 31 > qw || kt < w_full, met, lane);
+      wave_sync();
+      if (more) {
+        sk.store(mine[0], lane);
+        sv.store(mine[1], lane);
+      }
+    }
+    return met;
+  }
+
   // All keys of the block; whether an infinity or a NaN in a masked tile was met (GUARD: never).
   template <bool GUARD>
   __device__ __forceinline__ bool pass(Lds &lds, int tid, int lane) {
@@ -145,37 +198,31 @@ struct Dq {
   }
 };
 
+// The block's and the wave's part of the problem: queries q0 .. q0 + rows - 1, the wave's
+// from qw on; returns where the document of the block's last token starts.
 template <typename T, int DH, int BN>
-__global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 3 : 2) void attn_dq_kernel(AttnArgs a) {
-  using F = Dq<T, DH, BN>;
+__device__ __forceinline__ int begin(Dq<T, DH, BN> &f, const AttnArgs &a, int bh, int q0, int rows, int qw, int lane) {
   using TL = Tile<T, DH>;
-  __shared__ __align__(16) typename F::Lds lds;
-  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
-  int rank, bh;
-  block_of(a.B * a.H, rank, bh);
-  const int n_tiles = (a.T + 127) / 128;
-  const int b = bh / a.H, e = bh % a.H, g = e / (a.H / a.G);
-  F f;
-  f.q0 = (n_tiles - 1 - rank) * 128;
+  const int b = bh / a.H, e = bh % a.H, g = e / (a.H / a.G), h = lane >> 5;
+  f.q0 = q0;
   f.kh = a.k.p + b * a.k.batch + g * a.k.head;
   f.vh = a.v.p + b * a.v.batch + g * a.v.head;
   f.krow = a.k.row;
   f.vrow = a.v.row;
   f.hd = a.hd;
   f.c = a.scale * kLog2e;
-  f.qw = f.q0 + wave * 32;
+  f.qw = qw;
   f.limit = uniform(tokens_in_docs(a.cu, a.n_seqs, a.T));
-  const int q = f.qw + (lane & 31);
+  const int q = qw + (lane & 31);
   f.q = q;
-  int tail, unused;  // tail: where the document of the block's last token starts
+  int tail, unused;
   doc_of(a.cu, a.n_seqs, a.T, q, f.start, unused);
-  doc_of(a.cu, a.n_seqs, a.T, f.q0, f.first, unused);
+  doc_of(a.cu, a.n_seqs, a.T, q0, f.first, unused);
   f.first = uniform(f.first);
-  f.last = min(f.q0 + 127, f.limit - 1);
+  f.last = min(q0 + rows - 1, f.limit - 1);
   doc_of(a.cu, a.n_seqs, a.T, f.last, tail, unused);
-  tail = uniform(tail);
   f.w_first = uniform(f.start);  // (lane 0 has the lowest start)
-  f.w_full = full_from(f.start, f.qw, f.limit);
+  f.w_full = full_from(f.start, qw, f.limit);
 
   // a token of no document contributes nothing, whatever its rows hold
   const bool there = q < f.limit;
@@ -201,23 +248,82 @@ __global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 3 : 2) void attn_
     const float v = a.lse[(int64_t)bh * a.T + q];
     if (v != -INFINITY) f.lse2 = v * kLog2e;
   }
-  // Rows with few keys take delta = sum_j p (do . v_j) instead: o carries a rounding (2^-8 with
-  // bf16) that ds = p (do . v - delta) does not forgive where a few keys share the weight (two
-  // tokens of head_dim 16: dq 1.2 % off), while over many keys |o| falls below |v| and the
-  // error with it.  Done for rows whose document starts in the block (at most 128 keys),
-  // which costs blocks without such a start nothing.
-  if (f.first <= f.last && tail >= f.q0) {
-    const float d = f.delta_of_block(lds, tid, lane);
-    if (f.start >= f.q0) f.delta = d;
-  }
-  if (q < a.T && h == 0) a.delta[(int64_t)bh * a.T + q] = f.delta;
-
   asm volatile("" : "+v"(f.lse2));
+  return uniform(tail);
+}
+
+// Rows with few keys take delta = sum_j p (do . v_j) instead of do . o: o carries a rounding
+// (2^-8 with bf16) that ds = p (do . v - delta) does not forgive where a few keys share the
+// weight (two tokens of head_dim 16: dq 1.2 % off), while over many keys |o| falls below
+// |v| and the error with it.  Done for rows whose document starts among the last 128 keys of
+// the block, which costs blocks without such a start nothing.
+template <typename T, int DH, int BN>
+__global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 3 : 2) void attn_dq_kernel(AttnArgs a) {
+  using F = Dq<T, DH, BN>;
+  __shared__ __align__(16) typename F::Lds lds;
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
+  int rank, bh;
+  block_of(a.B * a.H, rank, bh);
+  const int q0 = ((a.T + 127) / 128 - 1 - rank) * 128;
+  F f;
+  const int tail = begin(f, a, bh, q0, 128, q0 + wave * 32, lane);
+  if (f.first <= f.last && tail >= q0) {
+    const float d = f.delta_of_block(lds, tid, lane);
+    if (f.start >= q0) f.delta = d;
+  }
+  if (f.q < a.T && h == 0) a.delta[(int64_t)bh * a.T + f.q] = f.delta;
+
   const bool met = f.template pass<false>(lds, tid, lane);
   if (__builtin_expect(__syncthreads_or(met), 0)) f.template pass<true>(lds, tid, lane);
-  if (!there) f.clear();
-  if (q < a.T)
-    write_row<T, DH>(a.dq.p + b * a.dq.batch + e * a.dq.head + (int64_t)q * a.dq.row, f.acc, a.scale, a.hd, lane);
+  if (f.q >= f.limit) f.clear();
+  if (f.q < a.T)
+    write_row<T, DH>(a.dq.p + bh / a.H * a.dq.batch + bh % a.H * a.dq.head + (int64_t)f.q * a.dq.row, f.acc, a.scale,
+                     a.hd, lane);
+}
+
+template <typename T, int DH>
+__global__ __launch_bounds__(256, 2) void attn_dq_few_kernel(AttnArgs a) {
+  using F = Dq<T, DH, 32>;
+  __shared__ __align__(16) FewLds<T, DH> lds;
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
+  int rank, bh;
+  block_of(a.B * a.H, rank, bh);
+  const int q0 = ((a.T + 31) / 32 - 1 - rank) * 32;
+  F f;
+  const int tail = begin(f, a, bh, q0, 32, q0, lane);
+  const int from = max(f.first, q0 - 96);
+  if (f.first <= f.last && tail >= from) {
+    const int kt = from + 32 * wave;
+    const float d = kt <= f.last ? f.delta_of_tile(lds.tile[wave], kt, lane) : 0.f;
+    if (h == 0) lds.tot[wave][lane] = d;
+    __syncthreads();
+    if (f.start >= from) {
+      const int i = lane & 31;
+      f.delta = (lds.tot[0][i] + lds.tot[1][i]) + (lds.tot[2][i] + lds.tot[3][i]);
+    }
+  }
+  if (f.q < a.T && h == 0 && wave == 0) a.delta[(int64_t)bh * a.T + f.q] = f.delta;
+
+  const bool met = f.template pass_few<false>(lds.tile[wave], wave, lane);
+  if (__builtin_expect(__syncthreads_or(met), 0)) f.template pass_few<true>(lds.tile[wave], wave, lane);
+  __syncthreads();  // (the sums take the tiles' place)
+#pragma unroll
+  for (int d = 0; d < F::TL::ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) lds.sum[wave][16 * d + i][lane] = f.acc[d][i];
+  __syncthreads();
+  if (f.q >= a.T) return;
+  for (int d = wave; d < F::TL::ND; d += 4) {
+    f32x16 x;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 16 * d + i;
+      const float s = (lds.sum[0][r][lane] + lds.sum[1][r][lane]) + (lds.sum[2][r][lane] + lds.sum[3][r][lane]);
+      x[i] = f.q < f.limit ? s : 0.f;
+    }
+    write_part<T>(a.dq.p + bh / a.H * a.dq.batch + bh % a.H * a.dq.head + (int64_t)f.q * a.dq.row, x, d, a.scale,
+                  a.hd, lane);
+  }
 }
 
 template <typename T, int DH, int BN>
@@ -547,10 +653,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   }
 }
 
-template <typename T, int DH, int BN>
+template <typename T, int DH, int BN, bool FEW = true>
 int launch(const AttnArgs &a, hipStream_t st) {
   const int n = (a.T + 127) / 128;
-  attn_dq_kernel<T, DH, BN><<<dim3(n * a.H * a.B), dim3(256), 0, st>>>(a);
+  bool few = false;
+  if constexpr (FEW) {
+    few = few_blocks(a);
+    if (few) attn_dq_few_kernel<T, DH><<<dim3((a.T + 31) / 32 * a.H * a.B), dim3(256), 0, st>>>(a);
+  }
+  if (!few) attn_dq_kernel<T, DH, BN><<<dim3(n * a.H * a.B), dim3(256), 0, st>>>(a);
   attn_dkv_kernel<T, DH, BN><<<dim3(n * a.G * a.n_split * a.B), dim3(256), 0, st>>>(a);
   if (a.n_split > 1) {
     const int64_t work = 2 * (int64_t)a.B * a.G * a.T * (a.hd / 4);

@@ -8,7 +8,7 @@ namespace dynconv {
 int attn_bwd_splits(int64_t B, int64_t T, int H, int G) {
   const int64_t blocks = (T + 127) / 128 * G * B, steps = (T + 63) / 64 * (H / G);
   const int64_t want = (1024 + blocks - 1) / blocks;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, steps / 2, 8}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, steps, 16}));
 }
 
 int attn_bwd(const AttnArgs &a, int dtype, hipStream_t st) {

@@ -240,3 +240,72 @@ def test_empty():
     g = dc.dynconv_attn_bwd(q, q, q, o, lse, q)
     torch.cuda.synchronize()
     assert lse.shape == (2, 4, 0) and g["dk"].shape == q.shape
+
+
+# Enough blocks of 128 queries for the chip (the shapes above have fewer and take blocks of 32).
+LARGE = [
+    (16, 260, 8, 2, 128),
+    (32, 130, 12, 12, 64),
+    (22, 129, 6, 3, 16),
+    (13, 385, 7, 1, 96),
+    (2, 2100, 8, 4, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", LARGE, ids=lambda s: "x".join(map(str, s)))
+def test_many_blocks_against_definition(shape, dtype):
+    _note(f"[attn] {shape} {dtype}")
+    q, k, v, d_o = _row(*shape, dtype, seed=sum(shape))
+    _compare(_run(q, k, v, d_o), au.attention(q, k, v, d_o=d_o), dtype)
+
+
+LONG_ROW = [0, 0, 1, 40, 171, 171, 300, 1500, 1564, 1628, 1700, 4100]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("heads", [(8, 2, 128), (9, 3, 64), (12, 12, 24)], ids=str)
+def test_many_blocks_packed(heads, dtype):
+    H, G, hd = heads
+    _note(f"[attn] long packed row {heads} {dtype}")
+    q, k, v, d_o = _row(1, 4200, H, G, hd, dtype, seed=H)
+    got = _run(q, k, v, d_o, cu=LONG_ROW)
+    _compare(got, au.attention(q, k, v, cu=LONG_ROW, d_o=d_o), dtype)
+    for n in ("o", "dq", "dk", "dv"):
+        assert bool((got[n][:, 4100:] == 0).all()), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("bad", BAD, ids=str)
+def test_many_blocks_masked_places(bad, hd, dtype):
+    _note(f"[attn] {bad} in masked places of a long row {hd} {dtype}")
+    cu = [0, 700, 760, 2500, 4100]
+    q, k, v, d_o = _row(1, 4200, 8, 4, hd, dtype, seed=17)
+    want = _run(q, k, v, d_o, cu=cu)
+    q2, k2, v2, d2 = (t.clone() for t in (q, k, v, d_o))
+    for t in (q2, k2, v2, d2):
+        t[:, 700:760] = bad
+        t[:, 4100:] = bad
+    got = _run(q2, k2, v2, d2, cu=cu)
+    for n in ("o", "dq", "dk", "dv"):
+        assert torch.equal(got[n][:, :700], want[n][:, :700]), n
+        assert torch.equal(got[n][:, 760:4100], want[n][:, 760:4100]), n
+        assert bool((got[n][:, 4100:] == 0).all()), n
+    v3 = v.clone()
+    v3[:, 1000:1100] = bad
+    got = _run(q, k, v3, d_o, cu=cu)
+    assert torch.equal(got["o"][:, :1000], want["o"][:, :1000])
+
+
+def test_seen_infinities():
+    """What a row does see of them it keeps: +infinity, -infinity or NaN as in the sum itself."""
+    _note("[attn] seen infinities")
+    for T, H in ((200, 2), (4200, 8)):
+        q, k, v, _ = _row(1, T, H, H, 64, "fp32", seed=19)
+        v[:, 50, :, 0], v[:, 60, :, 0], v[:, 70, :, 1], v[:, 80, :, 2] = math.inf, -math.inf, math.nan, -math.inf
+        ref = au.attention(q, k, v)["o"]
+        got = dc.dynconv_attn_fwd(q, k, v)
+        assert au.rel(got, ref) <= au.TOL["fp32"]
+        assert bool(torch.isinf(got[:, 50:60, :, 0]).all()) and bool(torch.isnan(got[:, 60:, :, 0]).all())
+        assert bool(torch.isfinite(got[:, :50]).all())
