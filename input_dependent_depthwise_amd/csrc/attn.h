@@ -398,12 +398,17 @@ __device__ __forceinline__ void write_row(char *row, const f32x16 (&acc)[DH / 32
   for (int d = 0; d < DH / 32; ++d) write_part<T>(row, acc[d], d, f, hd, lane);
 }
 
-// With fewer than one block of 128 queries for a CU, the chip waits for the longest chain of
+// With no more than one block of 128 queries for a CU the chip waits for the longest chain of
 // keys.  The forward and dq then take blocks of 32 queries whose 4 waves share the keys, every
 // fourth tile of 32 each in LDS of its own, and join their sums at the end: four times the
-// blocks, a quarter of the chain.
+// blocks, a quarter of the chain.  bf16, forward, without and with: 12 heads of 64, 1024 tokens
+// (96 blocks) 20 and 11 us; 8 of 128, 4096 (256) 87 and 74; 16 of 128, 4096 (512) 103 and 124;
+// 16 rows of 128 tokens, 12 of 64 (192): 8.1 and 9.9, a chain too short to be worth a join.
 constexpr int kFewBlocks = 256;
-inline bool few_blocks(const AttnArgs &a) { return (int64_t)((a.T + 127) / 128) * a.H * a.B < kFewBlocks; }
+inline bool few_blocks(const AttnArgs &a) {
+  const int64_t blocks = (int64_t)((a.T + 127) / 128) * a.H * a.B;
+  return blocks <= kFewBlocks && blocks <= a.T / 2;
+}
 
 template <typename T, int DH>
 struct FewLds {
@@ -438,6 +443,6 @@ int attn_fwd(const AttnArgs &a, int dtype, hipStream_t st);
 int attn_bwd(const AttnArgs &a, int dtype, hipStream_t st);
 int attn_bwd_fp32(const AttnArgs &a, hipStream_t st);
 // blocks that share the (query head, query tile) pairs of a tile of keys in the dk/dv kernel
-int attn_bwd_splits(int64_t B, int64_t T, int H, int G);
+int attn_bwd_splits(int64_t B, int64_t T, int H, int G, int dtype, bool packed);
 
 }  // namespace dynconv
