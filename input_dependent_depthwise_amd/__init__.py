@@ -412,6 +412,15 @@ def _new(like: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
+def _out(t, like: torch.Tensor, what: str, shape, dtype):
+    """An output and its View: the caller's, or a new contiguous one of like's shape."""
+    if t is not None:
+        return t, _pack_view(t, what, shape, dtype)
+    t = _new(like)
+    row = shape[-2] * shape[-1]
+    return t, _VIEW(t.data_ptr(), shape[1] * row if len(shape) == 4 else row, row, shape[-1])
+
+
 def dynconv_rope_freqs(rot_dim: int, base: float = 10000.0, *, stretch: float = 1.0, trained_len: float = 0.0,
                        slow_turns: float = 1.0, fast_turns: float = 32.0, device="cuda") -> torch.Tensor:
     """The frequencies of a rotary plan, float64 [rot_dim/2] on ``device``.
@@ -436,10 +445,9 @@ def dynconv_rope(x, freqs, *, positions=None, cu_seqlens=None, interleaved=False
     dt = x.dtype
     a = _pack_attn(B, T, H, 1, hd, dt, None, cu_seqlens)
     r = _pack_rotary(freqs, interleaved, inverse, factor)
-    if out is None:
-        out = _new(x)
-    rc = lib().dynconv_rope(a, r, _pack_view(x, "x", shape, dt), _int32(positions, "positions", (B, T)),
-                            _pack_view(out, "out", shape, dt), _raw_stream(x, stream))
+    vx = _pack_view(x, "x", shape, dt)
+    out, vy = _out(out, x, "out", shape, dt)
+    rc = lib().dynconv_rope(a, r, vx, _int32(positions, "positions", (B, T)), vy, _raw_stream(x, stream))
     if rc:
         _check(rc, "dynconv_rope")
     return out
@@ -453,13 +461,17 @@ def dynconv_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, o=None, lse=None, 
     B, T, H, hd = shape = _dims(q, "q", 4)
     G, dt = _dims(k, "k", 4)[2], q.dtype
     kv = (B, T, G, hd)
-    if o is None:
-        o = _new(q)
-    if lse is None and want_lse:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
-    rc = lib().dynconv_attn_fwd(_pack_attn(B, T, H, G, hd, dt, scale, cu_seqlens), _pack_view(q, "q", shape, dt),
-                                _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt), _pack_view(o, "o", shape, dt),
-                                None if lse is None else _lse(lse, (B, H, T)), _raw_stream(q, stream))
+    a, vq = _pack_attn(B, T, H, G, hd, dt, scale, cu_seqlens), _pack_view(q, "q", shape, dt)
+    o, vo = _out(o, q, "o", shape, dt)
+    if lse is not None:
+        pl = _lse(lse, (B, H, T))
+    elif want_lse:
+        lse = q.new_empty((B, H, T), dtype=torch.float32)
+        pl = lse.data_ptr()
+    else:
+        pl = None
+    rc = lib().dynconv_attn_fwd(a, vq, _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt), vo, pl,
+                                _raw_stream(q, stream))
     if rc:
         _check(rc, "dynconv_attn_fwd")
     return (o, lse) if want_lse else o
@@ -473,20 +485,20 @@ def dynconv_attn_bwd(q, k, v, o, lse, d_o, *, scale=None, cu_seqlens=None, out=N
     G, dt = _dims(k, "k", 4)[2], q.dtype
     kv = (B, T, G, hd)
     a = _pack_attn(B, T, H, G, hd, dt, scale, cu_seqlens)
-    g = dict(out or {})
-    for name, t in (("dq", q), ("dk", k), ("dv", v)):
-        if name not in g:
-            g[name] = _new(t)
+    ins = (_pack_view(q, "q", shape, dt), _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt),
+           _pack_view(o, "o", shape, dt), _lse(lse, (B, H, T)), _pack_view(d_o, "d_o", shape, dt))
+    out = out or {}
+    dq, vdq = _out(out.get("dq"), q, "dq", shape, dt)
+    dk, vdk = _out(out.get("dk"), k, "dk", kv, dt)
+    dv, vdv = _out(out.get("dv"), v, "dv", kv, dt)
     L = lib()
-    ws = _workspace(L.dynconv_attn_bwd_workspace_bytes(a), q.device, workspace)
-    rc = L.dynconv_attn_bwd(
-        a, _pack_view(q, "q", shape, dt), _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt),
-        _pack_view(o, "o", shape, dt), _lse(lse, (B, H, T)), _pack_view(d_o, "d_o", shape, dt),
-        _pack_view(g["dq"], "dq", shape, dt), _pack_view(g["dk"], "dk", kv, dt), _pack_view(g["dv"], "dv", kv, dt),
-        ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(q, stream))
+    ws = workspace
+    if ws is None:
+        ws = q.new_empty(L.dynconv_attn_bwd_workspace_bytes(a) or 1, dtype=torch.uint8)
+    rc = L.dynconv_attn_bwd(a, *ins, vdq, vdk, vdv, ws.data_ptr(), ws.nbytes, _raw_stream(q, stream))
     if rc:
         _check(rc, "dynconv_attn_bwd")
-    return g
+    return {"dq": dq, "dk": dk, "dv": dv}
 
 
 def dynconv_attn_decode(q, k, v, k_cache, v_cache, lengths, *, scale=None, freqs=None, interleaved=False, factor=1.0,
@@ -501,16 +513,16 @@ def dynconv_attn_decode(q, k, v, k_cache, v_cache, lengths, *, scale=None, freqs
     G, dt, cap = _dims(k, "k", 3)[1], q.dtype, _dims(k_cache, "k_cache", 4)[1]
     kv, rows = (B, G, hd), (B, cap, G, hd)
     a = _pack_attn(B, 1, H, G, hd, dt, scale, None)
-    if o is None:
-        o = _new(q)
+    vq = _pack_view(q, "q", shape, dt)
+    o, vo = _out(o, q, "o", shape, dt)
     L = lib()
     nbytes = L.dynconv_attn_decode_workspace_bytes(a, cap)
     ws = _workspace(nbytes, q.device, workspace) if nbytes else None
     rc = L.dynconv_attn_decode(
-        a, None if freqs is None else _pack_rotary(freqs, interleaved, False, factor), _pack_view(q, "q", shape, dt),
+        a, None if freqs is None else _pack_rotary(freqs, interleaved, False, factor), vq,
         _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt), _pack_view(k_cache, "k_cache", rows, dt),
-        _pack_view(v_cache, "v_cache", rows, dt), cap, _int32(lengths, "lengths", (B,)), _pack_view(o, "o", shape, dt),
-        _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(q, stream))
+        _pack_view(v_cache, "v_cache", rows, dt), cap, _int32(lengths, "lengths", (B,)), vo, _ptr(ws),
+        0 if ws is None else ws.nbytes, _raw_stream(q, stream))
     if rc:
         _check(rc, "dynconv_attn_decode")
     return o

@@ -197,10 +197,11 @@ struct Stage {
     for (int i = 0; i < N; ++i) r[i] = buf_load16(rs, at + i * step);
   }
   __device__ __forceinline__ void store(unsigned char *t, int tid) const {
-    static_assert(THREADS / TL::NC % 4 == 0, "");  // (whole groups of rows, so that a constant takes one to the next)
+    constexpr int R = THREADS / TL::NC;  // rows from one load to the next: whole groups of four, or half a group
+    static_assert(R % 4 == 0 || R == 2, "");
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      *reinterpret_cast<uint4 *>(t + TL::at(tid / TL::NC, tid % TL::NC) + i * (THREADS / TL::NC / 4) * TL::FOUR) = r[i];
+      *reinterpret_cast<uint4 *>(t + TL::at(tid / TL::NC, tid % TL::NC) + i * R / 4 * TL::FOUR + i * R % 4 * TL::ROW) = r[i];
   }
 };
 
@@ -398,6 +399,14 @@ __device__ __forceinline__ void write_row(char *row, const f32x16 (&acc)[DH / 32
   for (int d = 0; d < DH / 32; ++d) write_part<T>(row, acc[d], d, f, hd, lane);
 }
 
+// Waves of the forward and dq kernels on a SIMD: as many as the registers of a wave allow (3 and not 2
+// for bf16 heads of 64: 12 heads, 8 rows of 2048 tokens, forward 81 -> 75 us; 1 for rows of 512 bytes,
+// whose owned rows alone take 128 registers).
+template <typename T, int DH>
+constexpr int waves() {
+  return sizeof(T) * DH > 256 ? 1 : sizeof(T) * DH == 128 && sizeof(T) == 2 ? 3 : 2;
+}
+
 // With no more than one block of 128 queries for a CU the chip waits for the longest chain of
 // keys.  The forward and dq then take blocks of 32 queries whose 4 waves share the keys, every
 // fourth tile of 32 each in LDS of its own, and join their sums at the end: four times the
@@ -443,6 +452,6 @@ int attn_fwd(const AttnArgs &a, int dtype, hipStream_t st);
 int attn_bwd(const AttnArgs &a, int dtype, hipStream_t st);
 int attn_bwd_fp32(const AttnArgs &a, hipStream_t st);
 // blocks that share the (query head, query tile) pairs of a tile of keys in the dk/dv kernel
-int attn_bwd_splits(int64_t B, int64_t T, int H, int G, int dtype, bool packed);
+int attn_bwd_splits(const AttnArgs &a, int dtype);
 
 }  // namespace dynconv

@@ -150,7 +150,7 @@ struct BwdPlan {
 };
 BwdPlan bwd_plan(const dynconv_attn *a) {
   BwdPlan p;
-  p.splits = attn_bwd_splits(a->B, a->T, a->n_heads, a->n_kv_heads, a->dtype, a->cu_seqlens != nullptr);
+  p.splits = attn_bwd_splits(attn_args(a), a->dtype);
   p.delta = pad256(a->B * a->n_heads * a->T * 4);
   p.part = p.splits > 1 ? (int64_t)2 * p.splits * a->B * a->n_kv_heads * a->T * a->head_dim * 4 : 0;
   return p;

@@ -258,7 +258,7 @@ __device__ __forceinline__ int begin(Dq<T, DH, BN> &f, const AttnArgs &a, int bh
 // |v| and the error with it.  Done for rows whose document starts among the last 128 keys of
 // the block, which costs blocks without such a start nothing.
 template <typename T, int DH, int BN>
-__global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 3 : 2) void attn_dq_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, (waves<T, DH>())) void attn_dq_kernel(AttnArgs a) {
   using F = Dq<T, DH, BN>;
   __shared__ __align__(16) typename F::Lds lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
@@ -282,7 +282,7 @@ __global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 3 : 2) void attn_
 }
 
 template <typename T, int DH>
-__global__ __launch_bounds__(256, 2) void attn_dq_few_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, sizeof(T) * DH > 256 ? 1 : 2) void attn_dq_few_kernel(AttnArgs a) {
   using F = Dq<T, DH, 32>;
   __shared__ __align__(16) FewLds<T, DH> lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
@@ -653,15 +653,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   }
 }
 
-template <typename T, int DH, int BN, bool FEW = true>
+template <typename T, int DH, int BN>
 int launch(const AttnArgs &a, hipStream_t st) {
   const int n = (a.T + 127) / 128;
-  bool few = false;
-  if constexpr (FEW) {
-    few = few_blocks(a);
-    if (few) attn_dq_few_kernel<T, DH><<<dim3((a.T + 31) / 32 * a.H * a.B), dim3(256), 0, st>>>(a);
-  }
-  if (!few) attn_dq_kernel<T, DH, BN><<<dim3(n * a.H * a.B), dim3(256), 0, st>>>(a);
+  if (few_blocks(a)) attn_dq_few_kernel<T, DH><<<dim3((a.T + 31) / 32 * a.H * a.B), dim3(256), 0, st>>>(a);
+  else attn_dq_kernel<T, DH, BN><<<dim3(n * a.H * a.B), dim3(256), 0, st>>>(a);
   attn_dkv_kernel<T, DH, BN><<<dim3(n * a.G * a.n_split * a.B), dim3(256), 0, st>>>(a);
   if (a.n_split > 1) {
     const int64_t work = 2 * (int64_t)a.B * a.G * a.T * (a.hd / 4);

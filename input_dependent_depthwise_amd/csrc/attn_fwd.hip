@@ -207,7 +207,7 @@ __device__ __forceinline__ void begin(F &f, const AttnArgs &a, int bh, int q0, i
 }
 
 template <typename T, int DH, int BN>
-__global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 3 : 2) void attn_fwd_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, (waves<T, DH>())) void attn_fwd_kernel(AttnArgs a) {
   using F = Fwd<T, DH, BN>;
   __shared__ __align__(16) typename F::Lds lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 3 : 2) void attn_
 }
 
 template <typename T, int DH>
-__global__ __launch_bounds__(256, 2) void attn_fwd_few_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, sizeof(T) * DH > 256 ? 1 : 2) void attn_fwd_few_kernel(AttnArgs a) {
   using F = Fwd<T, DH, 32>;
   __shared__ __align__(16) FewLds<T, DH> lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
@@ -280,13 +280,11 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_few_kernel(AttnArgs a) {
     a.lse[(int64_t)bh * a.T + f.q] = none ? -INFINITY : top * a.scale + __builtin_amdgcn_logf(l) * kLn2;
 }
 
-template <typename T, int DH, int BN, bool FEW = true>
+template <typename T, int DH, int BN>
 int launch(const AttnArgs &a, hipStream_t st) {
-  if constexpr (FEW) {
-    if (few_blocks(a)) {
-      attn_fwd_few_kernel<T, DH><<<dim3((a.T + 31) / 32 * a.H * a.B), dim3(256), 0, st>>>(a);
-      return DYNCONV_OK;
-    }
+  if (few_blocks(a)) {
+    attn_fwd_few_kernel<T, DH><<<dim3((a.T + 31) / 32 * a.H * a.B), dim3(256), 0, st>>>(a);
+    return DYNCONV_OK;
   }
   attn_fwd_kernel<T, DH, BN><<<dim3((a.T + 127) / 128 * a.H * a.B), dim3(256), 0, st>>>(a);
   return DYNCONV_OK;
@@ -297,8 +295,7 @@ int launch(const AttnArgs &a, hipStream_t st) {
 int attn_fwd(const AttnArgs &a, int dtype, hipStream_t st) {
   if (dtype == DYNCONV_BF16) return a.hd <= 64 ? launch<bf16, 64, 64>(a, st) : launch<bf16, 128, 64>(a, st);
   if (a.hd <= 32) return launch<float, 32, 64>(a, st);
-  // (a wave alone cannot hold the next tile of 32 rows of 512 bytes)
-  return a.hd <= 64 ? launch<float, 64, 32>(a, st) : launch<float, 128, 32, false>(a, st);
+  return a.hd <= 64 ? launch<float, 64, 32>(a, st) : launch<float, 128, 32>(a, st);
 }
 
 }  // namespace dynconv
