@@ -398,8 +398,16 @@ def _pack_rotary(freqs: torch.Tensor, interleaved, inverse, factor) -> bytes:
     return _ROTARY(2 * freqs.shape[0], 1 if interleaved else 0, 1 if inverse else 0, factor, freqs.data_ptr())
 
 
-def _raw_stream(t: torch.Tensor, stream) -> int:
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
+def _raw_stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _on(stream, call, *args, **kw):
+    """call(...) with `stream` (a torch stream or a raw one) current, so that what it allocates belongs to that
+    stream too and is not handed out again while the stream still uses it."""
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+    with torch.cuda.stream(s):
+        return call(*args, **kw)
 
 
 def _lse(lse, shape) -> int:
@@ -441,13 +449,16 @@ def dynconv_rope(x, freqs, *, positions=None, cu_seqlens=None, interleaved=False
     last axis) with its first 2 * len(freqs) elements turned, as a new tensor or
     into ``out`` (x itself: in place).  positions: int32 [B, T], or the token's
     index in its row or, with cu_seqlens, in its document.  inverse: the backward."""
+    if stream is not None:
+        return _on(stream, dynconv_rope, x, freqs, positions=positions, cu_seqlens=cu_seqlens, interleaved=interleaved,
+                   factor=factor, inverse=inverse, out=out)
     B, T, H, hd = shape = _dims(x, "x", 4)
     dt = x.dtype
     a = _pack_attn(B, T, H, 1, hd, dt, None, cu_seqlens)
     r = _pack_rotary(freqs, interleaved, inverse, factor)
     vx = _pack_view(x, "x", shape, dt)
     out, vy = _out(out, x, "out", shape, dt)
-    rc = lib().dynconv_rope(a, r, vx, _int32(positions, "positions", (B, T)), vy, _raw_stream(x, stream))
+    rc = lib().dynconv_rope(a, r, vx, _int32(positions, "positions", (B, T)), vy, _raw_stream(x))
     if rc:
         _check(rc, "dynconv_rope")
     return out
@@ -458,6 +469,8 @@ def dynconv_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, o=None, lse=None, 
     v [B, T, n_kv_heads, head_dim] (any strides with a contiguous last axis).
     Returns o (and lse, fp32 [B, n_heads, T], when want_lse).  scale: default
     1 / sqrt(head_dim).  cu_seqlens: packed documents (B must be 1)."""
+    if stream is not None:
+        return _on(stream, dynconv_attn_fwd, q, k, v, scale=scale, cu_seqlens=cu_seqlens, o=o, lse=lse, want_lse=want_lse)
     B, T, H, hd = shape = _dims(q, "q", 4)
     G, dt = _dims(k, "k", 4)[2], q.dtype
     kv = (B, T, G, hd)
@@ -471,7 +484,7 @@ def dynconv_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, o=None, lse=None, 
     else:
         pl = None
     rc = lib().dynconv_attn_fwd(a, vq, _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt), vo, pl,
-                                _raw_stream(q, stream))
+                                _raw_stream(q))
     if rc:
         _check(rc, "dynconv_attn_fwd")
     return (o, lse) if want_lse else o
@@ -481,6 +494,9 @@ def dynconv_attn_bwd(q, k, v, o, lse, d_o, *, scale=None, cu_seqlens=None, out=N
     """Backward of dynconv_attn_fwd from its inputs, o, lse and d_o.  Returns
     dict(dq, dk, dv); ``out`` may hold any of them (views of one gradient row,
     for instance)."""
+    if stream is not None:
+        return _on(stream, dynconv_attn_bwd, q, k, v, o, lse, d_o, scale=scale, cu_seqlens=cu_seqlens, out=out,
+                   workspace=workspace)
     B, T, H, hd = shape = _dims(q, "q", 4)
     G, dt = _dims(k, "k", 4)[2], q.dtype
     kv = (B, T, G, hd)
@@ -495,7 +511,7 @@ def dynconv_attn_bwd(q, k, v, o, lse, d_o, *, scale=None, cu_seqlens=None, out=N
     ws = workspace
     if ws is None:
         ws = q.new_empty(L.dynconv_attn_bwd_workspace_bytes(a) or 1, dtype=torch.uint8)
-    rc = L.dynconv_attn_bwd(a, *ins, vdq, vdk, vdv, ws.data_ptr(), ws.nbytes, _raw_stream(q, stream))
+    rc = L.dynconv_attn_bwd(a, *ins, vdq, vdk, vdv, ws.data_ptr(), ws.nbytes, _raw_stream(q))
     if rc:
         _check(rc, "dynconv_attn_bwd")
     return {"dq": dq, "dk": dk, "dv": dv}
@@ -509,6 +525,9 @@ def dynconv_attn_decode(q, k, v, k_cache, v_cache, lengths, *, scale=None, freqs
     rotary plan (freqs None: not), k and v stored in the caches' rows lengths[b],
     and o [B, n_heads, head_dim] returned.  A slot with lengths[b] < 0 (or a full
     one) is idle: its o is zero."""
+    if stream is not None:
+        return _on(stream, dynconv_attn_decode, q, k, v, k_cache, v_cache, lengths, scale=scale, freqs=freqs,
+                   interleaved=interleaved, factor=factor, o=o, workspace=workspace)
     B, H, hd = shape = _dims(q, "q", 3)
     G, dt, cap = _dims(k, "k", 3)[1], q.dtype, _dims(k_cache, "k_cache", 4)[1]
     kv, rows = (B, G, hd), (B, cap, G, hd)
@@ -522,7 +541,7 @@ def dynconv_attn_decode(q, k, v, k_cache, v_cache, lengths, *, scale=None, freqs
         a, None if freqs is None else _pack_rotary(freqs, interleaved, False, factor), vq,
         _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt), _pack_view(k_cache, "k_cache", rows, dt),
         _pack_view(v_cache, "v_cache", rows, dt), cap, _int32(lengths, "lengths", (B,)), vo, _ptr(ws),
-        0 if ws is None else ws.nbytes, _raw_stream(q, stream))
+        0 if ws is None else ws.nbytes, _raw_stream(q))
     if rc:
         _check(rc, "dynconv_attn_decode")
     return o
