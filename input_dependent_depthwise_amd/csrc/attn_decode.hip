@@ -291,12 +291,20 @@ __global__ __launch_bounds__(kWaves * 64, 1) void attn_decode_kernel(DecodeArgs 
 #pragma unroll
     for (int r = 0; r < 4; ++r) st.acc[j][r] = 0.f;
 
+  // the next group is on the way while this one is used, where the registers hold both (fp32 rows
+  // of 512 bytes: 128 registers a group; eight waves' loads keep the memory busy there)
+  constexpr bool AHEAD = sizeof(T) * DH <= 256;
   for (; row0 < stop; row0 += kWaves * kGroup) {
-    GP y;
     const int next = row0 + kWaves * kGroup;
-    if (next < stop) y.fetch(kc, vc, a.kc.row, a.vc.row, next, stop, a.hd, lane);
-    st.add(x, q, row0, stop, lane);
-    if (next < stop) x = y;
+    if constexpr (AHEAD) {
+      GP y;
+      if (next < stop) y.fetch(kc, vc, a.kc.row, a.vc.row, next, stop, a.hd, lane);
+      st.add(x, q, row0, stop, lane);
+      if (next < stop) x = y;
+    } else {
+      st.add(x, q, row0, stop, lane);
+      if (next < stop) x.fetch(kc, vc, a.kc.row, a.vc.row, next, stop, a.hd, lane);
+    }
   }
   if (split == 0 && wave == kWaves - 1) {  // the new token: a group of one key (its wave has the fewest others)
     GP y;
