@@ -116,17 +116,20 @@ __device__ __forceinline__ void mma_step(const uint4 &a, const uint4 &b, f32x16 
   }
 }
 
-// A tile of rows of DH elements in LDS, row-major with gaps: 64 bytes between the
-// rows of a group of four, 16 after the group.  Modulo the 256 bytes of the banks, the
-// rows of a group then start 64 bytes apart (a multiple of it), which the transposing reads need (4 rows
-// x 64 bytes for a half wave), and 16 consecutive rows in 16 different places, which
-// the reads by rows need (one 16-byte chunk each).  Gaps and not a permutation of the chunks: every read of
-// a tile is one lane address plus a constant (an XOR took 24 registers and as many adds a tile).
+// A tile of rows of DH elements in LDS, row-major with gaps, so that modulo the 256 bytes of
+// the banks the four rows of a group start 64 bytes apart (in some order), which the transposing
+// reads need (4 rows x 64 bytes for a half wave), and 16 consecutive rows in 16 different
+// places, which the reads by rows need (one 16-byte chunk each): a row takes an odd number of
+// 64-byte pieces and a group of four an odd number of chunks.  Gaps and not a permutation of the
+// chunks: every read of a tile is one lane address plus a constant (an XOR took 24 registers
+// and as many adds a tile).
 template <typename T, int DH>
 struct Tile {
   static constexpr int E = 16 / (int)sizeof(T);  // elements of a chunk
   static constexpr int NC = DH / E;              // chunks of a row
-  static constexpr int ROW = DH * (int)sizeof(T) + 64, FOUR = 4 * ROW - 64 + 16;  // bytes from row to row, group to group
+  static constexpr int ROW = (NC / 4 | 1) * 64;  // bytes from row to row
+  static constexpr int FOUR = ((3 * ROW / 16 + NC) | 1) * 16;  // from group to group
+  static_assert(NC % 4 == 0, "");
   static constexpr int KS = NC / 2;              // steps of a sum over DH
   static constexpr int PS = 32 / (2 * E);        // steps of a sum over 32 rows
   static constexpr int ND = DH / 32;
@@ -183,25 +186,27 @@ __device__ __forceinline__ int score_row(int i, int h) { return 8 * (i >> 2) + 4
 template <typename T, int DH, int ROWS, int THREADS>
 struct Stage {
   using TL = Tile<T, DH>;
-  static constexpr int N = ROWS * TL::NC / THREADS;
-  static_assert(ROWS * TL::NC % THREADS == 0 && THREADS % TL::NC == 0, "");
+  // lanes of a row: its chunks, or the next power of two (the lanes past them idle)
+  static constexpr int W = TL::NC <= 8 ? 8 : TL::NC <= 16 ? 16 : 32;
+  static constexpr int N = ROWS * W / THREADS, R = THREADS / W;  // loads of a thread, rows from one to the next
+  static_assert(ROWS * W % THREADS == 0 && THREADS % W == 0 && TL::NC <= W, "");
+  static_assert(R % 4 == 0 || R == 2, "");  // (whole groups of four, or half a group)
   uint4 r[N];
   __device__ __forceinline__ void fetch(const char *head, int64_t row_bytes, int row0, int limit, int hd, int tid) {
     const int64_t bytes = (int64_t)(limit - row0 - 1) * row_bytes + hd * (int)sizeof(T);
     const __amdgpu_buffer_rsrc_t rs =
         make_rsrc(head + (int64_t)row0 * row_bytes, (uint32_t)(bytes < (int64_t)kOutside ? bytes : (int64_t)kOutside));
-    const int chunk = tid % TL::NC;
-    const uint32_t at = chunk * TL::E < hd ? (uint32_t)(tid / TL::NC) * (uint32_t)row_bytes + chunk * 16u : kOutside;
-    const uint32_t step = (uint32_t)(THREADS / TL::NC) * (uint32_t)row_bytes;
+    const int chunk = tid % W;
+    const uint32_t at = chunk * TL::E < hd ? (uint32_t)(tid / W) * (uint32_t)row_bytes + chunk * 16u : kOutside;
+    const uint32_t step = (uint32_t)R * (uint32_t)row_bytes;
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = buf_load16(rs, at + i * step);
   }
   __device__ __forceinline__ void store(unsigned char *t, int tid) const {
-    constexpr int R = THREADS / TL::NC;  // rows from one load to the next: whole groups of four, or half a group
-    static_assert(R % 4 == 0 || R == 2, "");
+    if (TL::NC < W && tid % W >= TL::NC) return;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      *reinterpret_cast<uint4 *>(t + TL::at(tid / TL::NC, tid % TL::NC) + i * R / 4 * TL::FOUR + i * R % 4 * TL::ROW) = r[i];
+      *reinterpret_cast<uint4 *>(t + TL::at(tid / W, tid % W) + i * R / 4 * TL::FOUR + i * R % 4 * TL::ROW) = r[i];
   }
 };
 

@@ -410,38 +410,40 @@ struct Dkv {
       if (!(seen >> i & 1u)) p[i] = dp[i] = 0.f;
   }
 
-  // The queries of one tile, from qt on.  Its products come in groups of four steps: scores and do . v
+  // The queries of one tile, from qt on.  Its products come in groups of three or four steps: scores and do . v
   // of the first 32 queries, those of the next 32, the sums of the first, the sums of the
   // next.  With one wave on a SIMD nobody else fills the gaps, so each group reads the operands of the
   // one after it before its products, and the softmax of 32 queries runs beside the products of a later
   // group; the scheduling barriers keep this order (left alone, every product waited for its own read).
   __device__ __forceinline__ void tile(const unsigned char *ql, const unsigned char *dl, const float (&stat)[2][BN],
                                        int qt, bool masked, bool &met, int lane) {
-    constexpr int NB = BN / 32, GA = TL::KS / 4, GC = TL::PS * TL::ND / 4;  // blocks; groups of a score, of a sum
+    constexpr int NB = BN / 32, S = TL::KS % 4 == 0 ? 4 : 3;         // blocks; steps of a group
+    constexpr int GA = TL::KS / S, GC = TL::PS * TL::ND / S;          // groups of a score, of a sum
+    static_assert(GA * S == TL::KS && GC * S == TL::PS * TL::ND, "");
     constexpr int C0 = NB * 2 * GA, ALL = C0 + NB * 2 * GC;
     f32x16 p[NB], dp[NB];
     uint32_t seen[NB];
-    uint4 f[2][4];
-    auto read = [&](int g, uint4(&x)[4]) {
+    uint4 f[2][S];
+    auto read = [&](int g, uint4(&x)[S]) {
       if (g < C0) {
         const unsigned char *t = g / GA % 2 == 0 ? ql : dl;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = TL::rows(t, g / (2 * GA) * 32, g % GA * 4 + i, lane);
+        for (int i = 0; i < S; ++i) x[i] = TL::rows(t, g / (2 * GA) * 32, g % GA * S + i, lane);
       } else {
         g -= C0;
         const unsigned char *t = g / GC % 2 == 0 ? dl : ql;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = g % GC * 4 + i;
+        for (int i = 0; i < S; ++i) {
+          const int k = g % GC * S + i;
           x[i] = TL::cols(t, g / (2 * GC) * 32, k / TL::ND, k % TL::ND, lane);
         }
       }
     };
-    auto multiply = [&](int g, const uint4(&x)[4]) {
+    auto multiply = [&](int g, const uint4(&x)[S]) {
       if (g < C0) {
-        const int n = g / (2 * GA), s = g % GA * 4;
+        const int n = g / (2 * GA), s = g % GA * S;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < S; ++i) {
           if (g / GA % 2 == 0) mma_step<T>(x[i], kf[s + i], p[n]);
           else mma_step<T>(x[i], vf[s + i], dp[n]);
         }
@@ -449,8 +451,8 @@ struct Dkv {
         g -= C0;
         const int n = g / (2 * GC);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = g % GC * 4 + i;
+        for (int i = 0; i < S; ++i) {
+          const int k = g % GC * S + i;
           if (g / GC % 2 == 0) mma_step<T>(x[i], score_frag<T>(p[n], k / TL::ND), av[k % TL::ND]);
           else mma_step<T>(x[i], score_frag<T>(dp[n], k / TL::ND), ak[k % TL::ND]);
         }
@@ -608,7 +610,7 @@ __global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 2 : 1) void attn_
     f.kf[s] = owned_chunk<T, DH>(krow, there, 2 * s + h, a.hd);
     f.vf[s] = owned_chunk<T, DH>(vrow, there, 2 * s + h, a.hd);
   }
-  if constexpr (DH == 128) {
+  if constexpr (DH > 64) {
     arrived_acc(f.kf);
     arrived_acc(f.vf);
   } else {

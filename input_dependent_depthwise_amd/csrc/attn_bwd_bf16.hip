@@ -11,7 +11,7 @@ namespace dynconv {
 // 54, 69.
 int attn_bwd_splits(const AttnArgs &a, int dtype) {
   const double blocks = (double)((a.T + 127) / 128) * a.G * a.B, tiles = (double)((a.T + 63) / 64) * (a.H / a.G);
-  const double tile_us = (dtype == DYNCONV_BF16 ? 1.0 : 8.0) * (a.hd <= 64 ? 1.4 : 2.8);
+  const double tile_us = (dtype == DYNCONV_BF16 ? 1.0 : 8.0) * (a.hd <= 64 ? 1.4 : a.hd <= 96 ? 2.1 : 2.8);
   const double split_us = 16.0 * a.B * a.T * a.G * a.hd / 4.5e6, join_us = 4.0;
   int best = 1;
   double least = tiles * tile_us;
@@ -25,9 +25,11 @@ int attn_bwd_splits(const AttnArgs &a, int dtype) {
   return best;
 }
 
+// (Heads of 80 on 96 columns against 128, 16 + 4 heads, 4 rows of 4096 tokens: 868 against 1010 us.)
 int attn_bwd(const AttnArgs &a, int dtype, hipStream_t st) {
   if (dtype != DYNCONV_BF16) return attn_bwd_fp32(a, st);
-  return a.hd <= 64 ? launch<bf16, 64, 64>(a, st) : launch<bf16, 128, 64>(a, st);
+  if (a.hd <= 64) return launch<bf16, 64, 64>(a, st);
+  return a.hd <= 96 ? launch<bf16, 96, 64>(a, st) : launch<bf16, 128, 64>(a, st);
 }
 
 }  // namespace dynconv

@@ -3,9 +3,11 @@
 
 namespace dynconv {
 
+// (Heads of 80 on 96 columns against 128, 16 + 4 heads, 4 rows of 4096 tokens: 6560 against 8350 us.)
 int attn_bwd_fp32(const AttnArgs &a, hipStream_t st) {
   if (a.hd <= 32) return launch<float, 32, 64>(a, st);
-  return a.hd <= 64 ? launch<float, 64, 32>(a, st) : launch<float, 128, 32>(a, st);
+  if (a.hd <= 64) return launch<float, 64, 32>(a, st);
+  return a.hd <= 96 ? launch<float, 96, 32>(a, st) : launch<float, 128, 32>(a, st);
 }
 
 }  // namespace dynconv

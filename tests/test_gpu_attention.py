@@ -309,3 +309,38 @@ def test_seen_infinities():
         assert au.rel(got, ref) <= au.TOL["fp32"]
         assert bool(torch.isinf(got[:, 50:60, :, 0]).all()) and bool(torch.isnan(got[:, 60:, :, 0]).all())
         assert bool(torch.isfinite(got[:, :50]).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("heads", [(6, 2, 96), (3, 3, 72), (4, 1, 88), (2, 1, 104)], ids=str)
+@pytest.mark.parametrize("docs", [PACKED[3], PACKED[5], (LONG_ROW, 4200)], ids=["300", "700", "4100"])
+def test_packed_heads_between_64_and_128(docs, heads, dtype):
+    cu, T = docs
+    H, G, hd = heads
+    if T > 1000:  # enough blocks of 128
+        H, G = 9 * G, 3 * G
+    _note(f"[attn] packed {len(cu) - 1} documents T={T} {H} {G} {hd} {dtype}")
+    q, k, v, d_o = _row(1, T, H, G, hd, dtype, seed=T + hd)
+    got = _run(q, k, v, d_o, cu=cu)
+    _compare(got, au.attention(q, k, v, cu=cu, d_o=d_o), dtype)
+    for n in ("o", "dq", "dk", "dv"):
+        assert bool((got[n][:, cu[-1]:] == 0).all()), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [333, 4200])
+@pytest.mark.parametrize("bad", BAD, ids=str)
+def test_masked_places_heads_of_96(bad, T, dtype):
+    _note(f"[attn] {bad} in masked places, heads of 96, {T} tokens {dtype}")
+    a, b, c = T // 6, T // 6 + 40, T - T // 40
+    q, k, v, d_o = _row(1, T, 9, 3, 96, dtype, seed=T)
+    want = _run(q, k, v, d_o, cu=[0, a, b, c])
+    q2, k2, v2, d2 = (t.clone() for t in (q, k, v, d_o))
+    for t in (q2, k2, v2, d2):
+        t[:, a:b] = bad
+        t[:, c:] = bad
+    got = _run(q2, k2, v2, d2, cu=[0, a, b, c])
+    for n in ("o", "dq", "dk", "dv"):
+        assert torch.equal(got[n][:, :a], want[n][:, :a]), n
+        assert torch.equal(got[n][:, b:c], want[n][:, b:c]), n
+        assert bool((got[n][:, c:] == 0).all()), n
