@@ -353,8 +353,9 @@ typedef struct {
  * scale: the factor on q.k, 0 for 1 / sqrt(head_dim); it must be finite and
  * not negative.  cu_seqlens / n_seqs: packed documents as in dynconv_problem
  * (B must be 1); tokens from cu_seqlens[n_seqs] on, if there are any, belong
- * to no document.  Limits: T and B below 2^31, B * n_heads * ceil(T / 64) below
- * 2^31, a row stride of at most 16 MiB. */
+ * to no document.  Limits: T and B below 2^31, B * n_heads * ceil(T / 128) below
+ * 2^24 (blocks of 256 threads, less than 2^32 threads in a launch), a row
+ * stride of at most 16 MiB. */
 typedef struct {
   int64_t B, T;
   int32_t n_heads, n_kv_heads, head_dim;
@@ -400,7 +401,8 @@ DYNCONV_API int dynconv_rope_freqs(int rot_dim, double base, double stretch, dou
  * in its row, or in its document with cu_seqlens (the padding counts on from
  * the last document's end).  y may be x's own view (in place); any other
  * overlap is refused.  Here head_dim and the strides may be any; a view of whole
- * 16-byte vectors with pairs that fill them takes the fast kernel.
+ * 16-byte vectors with pairs that fill them takes the fast kernel.  More work than
+ * 2^32 threads take in one launch is refused (DYNCONV_E_LIMIT).
  */
 DYNCONV_API int dynconv_rope(const dynconv_attn *a, const dynconv_rotary *r, const dynconv_view *x,
                              const int32_t *positions, const dynconv_view *y, hipStream_t stream);

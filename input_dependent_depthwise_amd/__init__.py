@@ -362,7 +362,7 @@ def _pack_view(t: torch.Tensor, what: str, shape, dtype) -> bytes:
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{what}: expected a {dtype} tensor on the GPU, got {t.dtype} on {t.device}")
     s = t.stride()
-    if s[-1] != 1 and shape[-1] > 1:
+    if s[-1] != 1 and shape[-1] > 1 and t.numel():
         raise ValueError(f"{what}: the last axis must be contiguous, got strides {s}")
     return _VIEW(t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else _VIEW(t.data_ptr(), s[0], 0, s[1])
 
@@ -383,12 +383,21 @@ def _int32(t, what: str, shape=None) -> int:
     return t.data_ptr()
 
 
+def _scale(scale) -> float:
+    """The factor on q.k as the struct has it, where 0 stands for the default."""
+    if scale is None:
+        return 0.0
+    if 0.0 <= scale < 2.0 ** -126:
+        raise ValueError(f"scale must be positive and no less than 2^-126, got {scale}")
+    return scale
+
+
 def _pack_attn(B, T, H, G, hd, dtype, scale, cu_seqlens) -> bytes:
     if cu_seqlens is None:
-        return _ATTN(B, T, H, G, hd, _dtype_code(dtype), scale or 0.0, 0, 0, 0)
+        return _ATTN(B, T, H, G, hd, _dtype_code(dtype), _scale(scale), 0, 0, 0)
     if cu_seqlens.dim() != 1:
         raise TypeError("cu_seqlens must be a contiguous 1-d int32 tensor")
-    return _ATTN(B, T, H, G, hd, _dtype_code(dtype), scale or 0.0, 0, _int32(cu_seqlens, "cu_seqlens"),
+    return _ATTN(B, T, H, G, hd, _dtype_code(dtype), _scale(scale), 0, _int32(cu_seqlens, "cu_seqlens"),
                  cu_seqlens.shape[0] - 1)
 
 
@@ -560,7 +569,7 @@ class QKVAttnFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, row, n_heads, n_kv_heads, freqs, interleaved=False, factor=1.0, scale=None, cu_seqlens=None):
         H, G = n_heads, n_kv_heads
-        heads = row.view(row.shape[0], row.shape[1], H + 2 * G, -1)
+        heads = row.view(row.shape[0], row.shape[1], H + 2 * G, row.shape[2] // (H + 2 * G))
         qk, v = heads[:, :, :H + G], heads[:, :, H + G:]
         if freqs is not None:
             qk = dynconv_rope(qk, freqs, cu_seqlens=cu_seqlens, interleaved=interleaved, factor=factor)

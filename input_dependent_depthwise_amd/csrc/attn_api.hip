@@ -105,7 +105,8 @@ int check_attn(const dynconv_attn *a, bool attention) {
     if (a->head_dim % (a->dtype == DYNCONV_BF16 ? 8 : 4) != 0) return DYNCONV_E_SHAPE;
     if (!(a->scale >= 0.f) || isinf(a->scale)) return DYNCONV_E_SHAPE;
     if (a->head_dim > 128) return DYNCONV_E_LIMIT;
-    if (a->B > 0 && a->T > 0 && (a->T + 63) / 64 > lim / a->n_heads / a->B) return DYNCONV_E_LIMIT;
+    // blocks of 256 threads, below 2^32 threads in all
+    if (a->B > 0 && a->T > 0 && (a->T + 127) / 128 > (((int64_t)1 << 24) - 1) / a->n_heads / a->B) return DYNCONV_E_LIMIT;
   }
   if (a->cu_seqlens) {
     if (a->B != 1 || a->n_seqs < 1) return DYNCONV_E_SHAPE;

@@ -160,8 +160,10 @@ int heads_per_thread(int64_t threads, int H) {
   return n;
 }
 
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;  // of 256 threads, below 2^32 threads in all
+
 template <typename T, int E>
-void launch(const RopeArgs &a, hipStream_t st) {
+int launch(const RopeArgs &a, hipStream_t st) {
   const int units = a.rot / (2 * E) + (a.in_place ? 0 : ((a.hd - a.rot) / E + 1) / 2);
   // tokens of a block: two units for a thread, no more than leave a block for every CU or fit
   // the block's pairs (four units, or two loaded before either is turned: 34.3 -> 36.3 us
@@ -169,15 +171,20 @@ void launch(const RopeArgs &a, hipStream_t st) {
   const int64_t all = (int64_t)a.B * a.T;
   const int64_t tokens = std::max<int64_t>(1, std::min<int64_t>({(512 + a.H * units - 1) / (a.H * units), all / 256,
                                                                  kPairs / (a.rot / 2)}));
-  rope_kernel<T, E><<<dim3((unsigned)((all + tokens - 1) / tokens)), dim3(256), 0, st>>>(a, units, (int)tokens);
+  const int64_t blocks = (all + tokens - 1) / tokens;
+  if (blocks > kMaxBlocks) return DYNCONV_E_LIMIT;
+  rope_kernel<T, E><<<dim3((unsigned)blocks), dim3(256), 0, st>>>(a, units, (int)tokens);
+  return DYNCONV_OK;
 }
 
 template <typename T>
-void launch_single(const RopeArgs &a, hipStream_t st) {
+int launch_single(const RopeArgs &a, hipStream_t st) {
   const int units = a.rot / 2 + (a.in_place ? 0 : a.hd - a.rot);
   const int64_t n = (int64_t)a.B * a.T * units;
   const int heads = heads_per_thread(n, a.H);
+  if ((n + 255) / 256 > kMaxBlocks) return DYNCONV_E_LIMIT;
   rope_single_kernel<T><<<dim3((unsigned)((n + 255) / 256), (a.H + heads - 1) / heads), dim3(256), 0, st>>>(a, units, heads);
+  return DYNCONV_OK;
 }
 
 }  // namespace
@@ -185,15 +192,11 @@ void launch_single(const RopeArgs &a, hipStream_t st) {
 int rope(const RopeArgs &a, int dtype, int vec_bytes, hipStream_t st) {
   if (a.rot > 2 * kPairs) vec_bytes = 0;
   if (dtype == DYNCONV_BF16) {
-    if (vec_bytes == 16) launch<bf16, 8>(a, st);
-    else if (vec_bytes == 8) launch<bf16, 4>(a, st);
-    else launch_single<bf16>(a, st);
-  } else {
-    if (vec_bytes == 16) launch<float, 4>(a, st);
-    else if (vec_bytes == 8) launch<float, 2>(a, st);
-    else launch_single<float>(a, st);
+    if (vec_bytes == 16) return launch<bf16, 8>(a, st);
+    return vec_bytes == 8 ? launch<bf16, 4>(a, st) : launch_single<bf16>(a, st);
   }
-  return DYNCONV_OK;
+  if (vec_bytes == 16) return launch<float, 4>(a, st);
+  return vec_bytes == 8 ? launch<float, 2>(a, st) : launch_single<float>(a, st);
 }
 
 }  // namespace dynconv

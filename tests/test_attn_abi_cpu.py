@@ -208,3 +208,19 @@ def test_binding_refuses_before_the_call():
         dc.dynconv_attn_fwd(x.half(), x.half(), x.half())
     with pytest.raises(dc.DynConvError):
         dc.dynconv_rope_freqs(5, device="cpu")
+
+
+def test_more_threads_than_a_launch_takes(L):
+    """2^24 blocks of 256 threads: refused before the launch."""
+    assert fwd(L, attn(B=1 << 14, T=128 << 7)) == LIMIT
+    assert L.dynconv_attn_bwd_workspace_bytes(ref(attn(B=1 << 14, T=128 << 7))) == 0
+    row = View(addr(0), 10 << 18, 10, 10)  # five pairs of single elements, a thread for each
+    r = Rotary(10, 0, 0, 1.0, 1 << 42)
+    assert rope(L, attn(B=1 << 12, T=1 << 18, n_heads=1, head_dim=10), r=r, x=row, y=row) == LIMIT
+
+
+def test_a_scale_of_zero_is_not_the_default():
+    assert dc._scale(None) == 0.0 and dc._scale(0.5) == 0.5
+    for s in (0, 0.0, 1e-39):
+        with pytest.raises(ValueError):
+            dc._scale(s)

@@ -88,3 +88,27 @@ def test_example():
     off, size = ex.decode()
     # two bf16 paths through projection, convolution, rotary and attention: some roundings of 2^-8 each
     assert off <= 8 * 2.0 ** -8 * size, (off, size)
+
+
+@pytest.mark.parametrize("B,T", [(2, 0), (0, 7)])
+def test_autograd_of_no_tokens(B, T):
+    print(f"[path] {B} rows of {T} tokens", flush=True)
+    freqs = dc.dynconv_rope_freqs(32, 10000.0).cuda()
+    row = torch.zeros(B, T, 4 * 32, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    o = dc.QKVAttnFn.apply(row, 2, 1, freqs)
+    assert o.shape == (B, T, 2, 32)
+    o.float().sum().backward()
+    assert row.grad.shape == row.shape
+
+
+def test_autograd_of_a_part_of_a_wider_row_and_a_broadcast_gradient():
+    print("[path] part of a wider row", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    freqs = dc.dynconv_rope_freqs(32, 10000.0).cuda()
+    wide = torch.randn(2, 77, 200, generator=g, device="cuda").bfloat16()
+    part, plain = wide[:, :, 40:168].requires_grad_(), wide[:, :, 40:168].contiguous().requires_grad_()
+    for row in (part, plain):
+        dc.QKVAttnFn.apply(row, 2, 1, freqs).sum().backward()  # d_o has strides of 0
+    assert torch.equal(part.grad, plain.grad)
+    with pytest.raises(ValueError):
+        dc.QKVAttnFn.apply(plain, 2, 1, freqs, False, 1.0, 0.0)
