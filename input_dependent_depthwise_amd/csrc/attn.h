@@ -364,6 +364,33 @@ __device__ __forceinline__ void sum_rows(const unsigned char *t, int r0, const f
   }
 }
 
+// acc += tile^T of what p loses when it is rounded to bf16 (KEPT: of the tile's finite values),
+// for the masked tiles of short rows: where few keys and queries meet, few roundings are
+// averaged.  bf16, 3 tokens, error of dq and dk against 64 bits over that of their own rounding: 1.4
+// (1.7 at worst) without it, 1.0 with it; at 1000 tokens 1.4 (1.5) in any case without it.
+template <bool KEPT, typename T, int DH>
+__device__ __forceinline__ void sum_rows_rest(const unsigned char *t, int r0, const f32x16 &p, f32x16 (&acc)[DH / 32],
+                                              int lane) {
+  using TL = Tile<T, DH>;
+  if constexpr (sizeof(T) == 2) {
+    f32x16 rest;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float x = p[i] - (float)(bf16)p[i];
+      rest[i] = x == x ? x : 0.f;  // (an infinite p)
+    }
+#pragma unroll
+    for (int s = 0; s < TL::PS; ++s) {
+      const uint4 b = score_frag<T>(rest, s);
+#pragma unroll
+      for (int d = 0; d < TL::ND; ++d) {
+        const uint4 x = TL::cols(t, r0, s, d, lane);
+        mma_step<T>(KEPT ? part_of<T, Part::KEEP>(x) : x, b, acc[d]);
+      }
+    }
+  }
+}
+
 // In a tile where some row is not seen by some owned row, a product with that pair's zero p would
 // carry an infinity or a NaN of the row to where it is not seen.  A kernel's first
 // pass (GUARD false) only notes that it met one in such a tile; its block then starts
@@ -422,6 +449,15 @@ constexpr int kFewBlocks = 256;
 inline bool few_blocks(const AttnArgs &a) {
   const int64_t blocks = (int64_t)((a.T + 127) / 128) * a.H * a.B;
   return blocks <= kFewBlocks && blocks <= a.T / 2;
+}
+
+// Rows short enough to take sum_rows_rest.  Its products and registers cost 4096 rows of 16 tokens
+// (12 heads of 64) 363 -> 385 us forward and 1262 -> 1432 backward, one row of 37 nothing; they would
+// cost packed rows of 16384 (heads of 128) 5 % of the forward, of 8192 15 % of forward and
+// backward, where the sums average the roundings.
+template <typename T>
+inline bool with_rest(const AttnArgs &a) {
+  return sizeof(T) == 2 && a.T <= 64;
 }
 
 template <typename T, int DH>

@@ -20,7 +20,7 @@ namespace dynconv {
 
 namespace {
 
-template <typename T, int DH, int BN>
+template <typename T, int DH, int BN, bool REST>
 struct Dq {
   using TL = Tile<T, DH>;
   typedef unsigned char Lds[2][2][TL::bytes(BN)];  // [buffer][key, value]
@@ -107,6 +107,7 @@ struct Dq {
       sum_rows<T, DH>(kl, 32 * n, p, acc, lane);
       if constexpr (sizeof(T) == 2) read_ahead<TL::PS * TL::ND, 2, 1, 4>();
     }
+    if (REST && masked) sum_rows_rest<GUARD, T, DH>(kl, 32 * n, p, acc, lane);
   }
 
   // As delta_of_block, one tile of 32 keys from kt on (a wave's share).
@@ -206,8 +207,8 @@ struct Dq {
 
 // The block's and the wave's part of the problem: queries q0 .. q0 + rows - 1, the wave's
 // from qw on; returns where the document of the block's last token starts.
-template <typename T, int DH, int BN>
-__device__ __forceinline__ int begin(Dq<T, DH, BN> &f, const AttnArgs &a, int bh, int q0, int rows, int qw, int lane) {
+template <typename T, int DH, int BN, bool REST>
+__device__ __forceinline__ int begin(Dq<T, DH, BN, REST> &f, const AttnArgs &a, int bh, int q0, int rows, int qw, int lane) {
   using TL = Tile<T, DH>;
   const int b = bh / a.H, e = bh % a.H, g = e / (a.H / a.G), h = lane >> 5;
   f.q0 = q0;
@@ -263,9 +264,9 @@ __device__ __forceinline__ int begin(Dq<T, DH, BN> &f, const AttnArgs &a, int bh
 // weight (two tokens of head_dim 16: dq 1.2 % off), while over many keys |o| falls below
 // |v| and the error with it.  Done for rows whose document starts among the last 128 keys of
 // the block, which costs blocks without such a start nothing.
-template <typename T, int DH, int BN>
+template <typename T, int DH, int BN, bool REST>
 __global__ __launch_bounds__(256, (waves<T, DH>())) void attn_dq_kernel(AttnArgs a) {
-  using F = Dq<T, DH, BN>;
+  using F = Dq<T, DH, BN, REST>;
   __shared__ __align__(16) typename F::Lds lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
   int rank, bh;
@@ -287,9 +288,9 @@ __global__ __launch_bounds__(256, (waves<T, DH>())) void attn_dq_kernel(AttnArgs
                      a.hd, lane);
 }
 
-template <typename T, int DH>
+template <typename T, int DH, bool REST>
 __global__ __launch_bounds__(256, sizeof(T) * DH > 256 ? 1 : 2) void attn_dq_few_kernel(AttnArgs a) {
-  using F = Dq<T, DH, 32>;
+  using F = Dq<T, DH, 32, REST>;
   __shared__ __align__(16) FewLds<T, DH> lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
   int rank, bh;
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(256, sizeof(T) * DH > 256 ? 1 : 2) void attn_dq_few
   }
 }
 
-template <typename T, int DH, int BN>
+template <typename T, int DH, int BN, bool REST>
 struct Dkv {
   using TL = Tile<T, DH>;
   static_assert(BN <= 64, "");
@@ -489,10 +490,17 @@ struct Dkv {
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if (REST && masked) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        sum_rows_rest<false, T, DH>(dl, 32 * n, p[n], av, lane);
+        sum_rows_rest<false, T, DH>(ql, 32 * n, dp[n], ak, lane);
+      }
+    }
   }
-  // The same for 32 queries, sums guarded where some query does not see some key.
+  // The same for 32 queries, sums guarded where some query does not see some key; or their rest.
   __device__ __forceinline__ void guarded(const unsigned char *ql, const unsigned char *dl,
-                                          const float (&stat)[2][BN], int n, int qt, int lane) {
+                                          const float (&stat)[2][BN], int n, int qt, bool rest, int lane) {
     f32x16 p, dp;
     begin(stat, n, p, dp, lane);
 #pragma unroll
@@ -503,8 +511,13 @@ struct Dkv {
 #pragma unroll
     for (int j = 0; j < 4; ++j) weights(stat, n, j, p, dp, lane);
     drop(seen, p, dp);
-    sum_rows_guarded<T, DH>(dl, 32 * n, p, seen, av, lane);
-    sum_rows_guarded<T, DH>(ql, 32 * n, dp, seen, ak, lane);
+    if (REST && rest) {
+      sum_rows_rest<true, T, DH>(dl, 32 * n, p, av, lane);
+      sum_rows_rest<true, T, DH>(ql, 32 * n, dp, ak, lane);
+    } else {
+      sum_rows_guarded<T, DH>(dl, 32 * n, p, seen, av, lane);
+      sum_rows_guarded<T, DH>(ql, 32 * n, dp, seen, ak, lane);
+    }
   }
 
   // The block's part of the (head, query tile) pairs, heads outside; returns as Dq::pass.
@@ -558,11 +571,15 @@ struct Dkv {
       if (more) fetch(e2, qt2);
       if (qt + BN > kw && kw < limit) {
         const unsigned char *ql = lds.tile[buf][0], *dl = lds.tile[buf][1];
+        const bool masked = qt < kw + 31 || qt + BN > w_end;
         if constexpr (GUARD) {
 #pragma unroll 1
-          for (int n = 0; n < BN / 32; ++n) guarded(ql, dl, lds.stat[buf], n, qt + 32 * n, lane);
+          for (int i = 0; i < (REST && masked ? 2 : 1) * (BN / 32); ++i) {  // (sums in tile()'s order)
+            const int n = i % (BN / 32);
+            guarded(ql, dl, lds.stat[buf], n, qt + 32 * n, i >= BN / 32, lane);
+          }
         } else {
-          tile(ql, dl, lds.stat[buf], qt, qt < kw + 31 || qt + BN > w_end, met, lane);
+          tile(ql, dl, lds.stat[buf], qt, masked, met, lane);
         }
       }
       if (more) store(buf ^ 1);
@@ -575,9 +592,9 @@ struct Dkv {
   }
 };
 
-template <typename T, int DH, int BN>
+template <typename T, int DH, int BN, bool REST>
 __global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(AttnArgs a) {
-  using F = Dkv<T, DH, BN>;
+  using F = Dkv<T, DH, BN, REST>;
   using TL = Tile<T, DH>;
   __shared__ __align__(16) typename F::Lds lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
@@ -661,17 +678,21 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   }
 }
 
-template <typename T, int DH, int BN>
-int launch(const AttnArgs &a, hipStream_t st) {
+template <typename T, int DH, int BN, bool REST>
+int launch_as(const AttnArgs &a, hipStream_t st) {
   const int n = (a.T + 127) / 128;
-  if (few_blocks(a)) attn_dq_few_kernel<T, DH><<<dim3((a.T + 31) / 32 * a.H * a.B), dim3(256), 0, st>>>(a);
-  else attn_dq_kernel<T, DH, BN><<<dim3(n * a.H * a.B), dim3(256), 0, st>>>(a);
-  attn_dkv_kernel<T, DH, BN><<<dim3(n * a.G * a.n_split * a.B), dim3(256), 0, st>>>(a);
+  if (few_blocks(a)) attn_dq_few_kernel<T, DH, REST><<<dim3((a.T + 31) / 32 * a.H * a.B), dim3(256), 0, st>>>(a);
+  else attn_dq_kernel<T, DH, BN, REST><<<dim3(n * a.H * a.B), dim3(256), 0, st>>>(a);
+  attn_dkv_kernel<T, DH, BN, REST><<<dim3(n * a.G * a.n_split * a.B), dim3(256), 0, st>>>(a);
   if (a.n_split > 1) {
     const int64_t work = 2 * (int64_t)a.B * a.G * a.T * (a.hd / 4);
     attn_join_kernel<T><<<dim3((unsigned)((work + 255) / 256)), dim3(256), 0, st>>>(a);
   }
   return DYNCONV_OK;
+}
+template <typename T, int DH, int BN>
+int launch(const AttnArgs &a, hipStream_t st) {
+  return with_rest<T>(a) ? launch_as<T, DH, BN, sizeof(T) == 2>(a, st) : launch_as<T, DH, BN, false>(a, st);
 }
 
 }  // namespace

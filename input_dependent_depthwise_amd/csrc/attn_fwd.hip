@@ -22,7 +22,7 @@ namespace {
 // take 82 (heads of 64, two waves), 128 took 123 (registers).
 constexpr float kSlack = 8.f;
 
-template <typename T, int DH, int BN>
+template <typename T, int DH, int BN, bool REST>
 struct Fwd {
   using TL = Tile<T, DH>;
   typedef unsigned char Lds[2][2][TL::bytes(BN)];  // [buffer][key, value]
@@ -112,6 +112,10 @@ struct Fwd {
         sum_rows<T, DH>(vl, 32 * n, p[n], acc, lane);
         if constexpr (sizeof(T) == 2) read_ahead<TL::PS * TL::ND, 2, 1, 4>();
       }
+    }
+    if (REST && masked) {
+#pragma unroll
+      for (int n = 0; n < BN / 32; ++n) sum_rows_rest<GUARD, T, DH>(vl, 32 * n, p[n], acc, lane);
     }
   }
 
@@ -212,9 +216,9 @@ __device__ __forceinline__ void begin(F &f, const AttnArgs &a, int bh, int q0, i
   arrived(f.qf);
 }
 
-template <typename T, int DH, int BN>
+template <typename T, int DH, int BN, bool REST>
 __global__ __launch_bounds__(256, (waves<T, DH>())) void attn_fwd_kernel(AttnArgs a) {
-  using F = Fwd<T, DH, BN>;
+  using F = Fwd<T, DH, BN, REST>;
   __shared__ __align__(16) typename F::Lds lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
   int rank, bh;
@@ -236,9 +240,9 @@ __global__ __launch_bounds__(256, (waves<T, DH>())) void attn_fwd_kernel(AttnArg
   }
 }
 
-template <typename T, int DH>
+template <typename T, int DH, bool REST>
 __global__ __launch_bounds__(256, sizeof(T) * DH > 256 ? 1 : 2) void attn_fwd_few_kernel(AttnArgs a) {
-  using F = Fwd<T, DH, 32>;
+  using F = Fwd<T, DH, 32, REST>;
   __shared__ __align__(16) FewLds<T, DH> lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
   int rank, bh;
@@ -286,14 +290,18 @@ __global__ __launch_bounds__(256, sizeof(T) * DH > 256 ? 1 : 2) void attn_fwd_fe
     a.lse[(int64_t)bh * a.T + f.q] = none ? -INFINITY : top * a.scale + __builtin_amdgcn_logf(l) * kLn2;
 }
 
-template <typename T, int DH, int BN>
-int launch(const AttnArgs &a, hipStream_t st) {
+template <typename T, int DH, int BN, bool REST>
+int launch_as(const AttnArgs &a, hipStream_t st) {
   if (few_blocks(a)) {
-    attn_fwd_few_kernel<T, DH><<<dim3((a.T + 31) / 32 * a.H * a.B), dim3(256), 0, st>>>(a);
+    attn_fwd_few_kernel<T, DH, REST><<<dim3((a.T + 31) / 32 * a.H * a.B), dim3(256), 0, st>>>(a);
     return DYNCONV_OK;
   }
-  attn_fwd_kernel<T, DH, BN><<<dim3((a.T + 127) / 128 * a.H * a.B), dim3(256), 0, st>>>(a);
+  attn_fwd_kernel<T, DH, BN, REST><<<dim3((a.T + 127) / 128 * a.H * a.B), dim3(256), 0, st>>>(a);
   return DYNCONV_OK;
+}
+template <typename T, int DH, int BN>
+int launch(const AttnArgs &a, hipStream_t st) {
+  return with_rest<T>(a) ? launch_as<T, DH, BN, sizeof(T) == 2>(a, st) : launch_as<T, DH, BN, false>(a, st);
 }
 
 }  // namespace

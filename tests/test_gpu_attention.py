@@ -344,3 +344,16 @@ def test_masked_places_heads_of_96(bad, T, dtype):
         assert torch.equal(got[n][:, :a], want[n][:, :a]), n
         assert torch.equal(got[n][:, b:c], want[n][:, b:c]), n
         assert bool((got[n][:, c:] == 0).all()), n
+
+
+@pytest.mark.parametrize("hd", [64, 96, 128])
+@pytest.mark.parametrize("B,T", [(1, 2), (1, 3), (40, 5), (1, 31), (30, 32)])
+def test_short_rows_in_bf16_lose_no_more_than_their_own_rounding(B, T, hd):
+    """p and ds enter the products with 16 bits there (2^-17 each, against 2^-9 of the outputs' rounding)."""
+    _note(f"[attn] own rounding {B} {T} {hd}")
+    q, k, v, d_o = _row(B, T, 4, 2, hd, "bf16", seed=B + T + hd)
+    got, ref = _run(q, k, v, d_o), au.attention(q, k, v, d_o=d_o)
+    for n in ("o", "dq", "dk", "dv"):
+        off = (got[n].double() - ref[n]).norm()
+        own = (ref[n].bfloat16().double() - ref[n]).norm()
+        assert off <= 1.1 * own + 2.0 ** -16 * ref[n].norm(), (n, float(off / own))
