@@ -14,6 +14,7 @@
 #pragma once
 
 #include "bufio.h"
+#include "docs.h"
 #include "mfma.h"
 
 namespace dynconv {
@@ -52,35 +53,6 @@ __device__ __forceinline__ void widen(const uint4 &r, float (&f)[16 / sizeof(T)]
       f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-}
-
-// Tokens of the row that belong to a document (all T without packing).
-__device__ __forceinline__ int tokens_in_docs(const int32_t *cu, int n_seqs, int T) {
-  if (!cu) return T;
-  return min(max(cu[n_seqs], 0), T);
-}
-
-// The document of token t: [start, end).  A token of none gets start > t and
-// end = 0.  Whatever the offsets hold, start >= 0 and end <= T.
-__device__ __forceinline__ void doc_of(const int32_t *cu, int n_seqs, int T, int t, int &start, int &end) {
-  if (!cu) {
-    start = t < T ? 0 : T;
-    end = t < T ? T : 0;
-    return;
-  }
-  int lo = 0, hi = n_seqs;  // the first j in [1, n_seqs] with cu[j] > t, else n_seqs + 1
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid + 1] > t) hi = mid;
-    else lo = mid + 1;
-  }
-  if (lo >= n_seqs || t >= T) {
-    start = T;
-    end = 0;
-    return;
-  }
-  start = min(max(cu[lo], 0), t);
-  end = min(cu[lo + 1], T);
 }
 
 // The key from which on every row of a wave (queries qw .. qw+31, start: the lane's) sees
@@ -179,7 +151,7 @@ __device__ __forceinline__ uint4 score_frag(const f32x16 &p, int s) {
 __device__ __forceinline__ int score_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 
 // Copies rows [row0, row0 + ROWS) of one head into a tile, through registers:
-// fetch() issues the loads, store() writes what came.  Rows at or past `limit` (> row0)
+// fetch() issues the loads, store() writes what came.  Rows at or past `limit`
 // and elements past head_dim come as zeros (of rows that overlap each other in
 // memory, rows past `limit` come as whatever rows before it hold; nothing depends on them):
 // the buffer ends with row limit - 1, so a load is one address sum.
@@ -193,9 +165,8 @@ struct Stage {
   static_assert(R % 4 == 0 || R == 2, "");  // (whole groups of four, or half a group)
   uint4 r[N];
   __device__ __forceinline__ void fetch(const char *head, int64_t row_bytes, int row0, int limit, int hd, int tid) {
-    const int64_t bytes = (int64_t)(limit - row0 - 1) * row_bytes + hd * (int)sizeof(T);
     const __amdgpu_buffer_rsrc_t rs =
-        make_rsrc(head + (int64_t)row0 * row_bytes, (uint32_t)(bytes < (int64_t)kOutside ? bytes : (int64_t)kOutside));
+        make_rsrc(head + (int64_t)row0 * row_bytes, rows_extent(row0, limit, row_bytes, hd * (int)sizeof(T), kOutside));
     const int chunk = tid % W;
     const uint32_t at = chunk * TL::E < hd ? (uint32_t)(tid / W) * (uint32_t)row_bytes + chunk * 16u : kOutside;
     const uint32_t step = (uint32_t)R * (uint32_t)row_bytes;

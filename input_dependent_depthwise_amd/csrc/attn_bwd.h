@@ -223,11 +223,10 @@ __device__ __forceinline__ int begin(Dq<T, DH, BN, REST> &f, const AttnArgs &a, 
   const int q = qw + (lane & 31);
   f.q = q;
   int tail, unused;
-  doc_of(a.cu, a.n_seqs, a.T, q, f.start, unused);
-  doc_of(a.cu, a.n_seqs, a.T, q0, f.first, unused);
+  doc_of(a.cu, a.n_seqs, a.T, f.limit, q, f.start, unused);
+  keys_of(a.cu, a.n_seqs, a.T, f.limit, q0, rows, f.first, f.last);
   f.first = uniform(f.first);
-  f.last = min(q0 + rows - 1, f.limit - 1);
-  doc_of(a.cu, a.n_seqs, a.T, f.last, tail, unused);
+  doc_of(a.cu, a.n_seqs, a.T, f.limit, f.last, tail, unused);
   f.w_first = uniform(f.start);  // (lane 0 has the lowest start)
   f.w_full = full_from(f.start, qw, f.limit);
 
@@ -614,9 +613,8 @@ __global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 2 : 1) void attn_
   const int key = f.kw + (lane & 31);
   f.key = key;
   int unused;
-  doc_of(a.cu, a.n_seqs, a.T, key, unused, f.end);
-  doc_of(a.cu, a.n_seqs, a.T, min(f.k0 + 127, f.limit - 1), unused, f.stop);
-  f.stop = uniform(f.k0 < f.limit ? f.stop : 0);
+  doc_of(a.cu, a.n_seqs, a.T, f.limit, key, unused, f.end);
+  f.stop = uniform(queries_end(a.cu, a.n_seqs, a.T, f.limit, f.k0, 128));
   f.w_end = __builtin_amdgcn_readlane(f.end, 0);  // (the wave's ends rise)
 
   const bool there = key < f.limit;

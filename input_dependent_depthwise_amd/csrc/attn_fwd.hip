@@ -204,10 +204,9 @@ __device__ __forceinline__ void begin(F &f, const AttnArgs &a, int bh, int q0, i
   const int q = qw + (lane & 31);
   f.q = q;
   int unused;
-  doc_of(a.cu, a.n_seqs, a.T, q, f.start, unused);
-  doc_of(a.cu, a.n_seqs, a.T, q0, f.first, unused);
+  doc_of(a.cu, a.n_seqs, a.T, f.limit, q, f.start, unused);
+  keys_of(a.cu, a.n_seqs, a.T, f.limit, q0, rows, f.first, f.last);
   f.first = uniform(f.first);
-  f.last = min(q0 + rows - 1, f.limit - 1);
   f.w_first = uniform(f.start);  // (lane 0 has the lowest start)
   f.w_full = full_from(f.start, qw, f.limit);
   const char *qrow = a.q.p + b * a.q.batch + e * a.q.head + (int64_t)q * a.q.row;

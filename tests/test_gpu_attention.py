@@ -357,3 +357,29 @@ def test_short_rows_in_bf16_lose_no_more_than_their_own_rounding(B, T, hd):
         off = (got[n].double() - ref[n]).norm()
         own = (ref[n].bfloat16().double() - ref[n]).norm()
         assert off <= 1.1 * own + 2.0 ** -16 * ref[n].norm(), (n, float(off / own))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd", [24, 64, 80, 128])
+@pytest.mark.parametrize("cu,T", [([0, 130, 100], 130), ([0, 40, 700, 90, 300], 520)], ids=["130", "520"])
+def test_offsets_that_fall_stay_inside_the_row(cu, T, hd, dtype):
+    """Offsets that break the rule give unspecified values, from the row's own tokens and into them alone."""
+    _note(f"[attn] falling offsets {cu} T={T} {hd} {dtype}")
+    H, G, room = 4, 2, 200
+    q, k, v, d_o = _row(1, T, H, G, hd, dtype, seed=T + hd)
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    seen = []
+    for around in (0.0, 5.0):
+        wide = [torch.full((1, T + 2 * room, t.shape[2], hd), around, dtype=t.dtype, device="cuda") for t in (q, k, v, d_o)]
+        for w, t in zip(wide, (q, k, v, d_o)):
+            w[:, room:room + T] = t
+        x = [w[:, room:room + T] for w in wide]
+        out = [torch.full_like(w, 7.0) for w in (wide[0], *wide[:3])]
+        o, dq, dk, dv = (w[:, room:room + T] for w in out)
+        _, lse = dc.dynconv_attn_fwd(*x[:3], cu_seqlens=c, o=o, want_lse=True)
+        dc.dynconv_attn_bwd(*x[:3], o, lse, x[3], cu_seqlens=c, out={"dq": dq, "dk": dk, "dv": dv})
+        torch.cuda.synchronize()
+        for w in out:
+            assert bool((w[:, :room] == 7).all()) and bool((w[:, room + T:] == 7).all())
+        seen.append([t.clone() for t in (o, lse, dq, dk, dv)])
+    assert all(torch.equal(a, b) for a, b in zip(*seen))
