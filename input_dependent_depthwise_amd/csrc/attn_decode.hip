@@ -17,8 +17,12 @@
 //
 // q (times scale and log2 e) and, for bf16 caches, the probabilities enter as
 // sums of two bf16 values, so their rounding does not show in o; the matrix
-// cores are idle enough for twice the products.
+// cores are idle enough for twice the products.  An infinity in the cache takes part in the
+// first of the two products alone (times a second part of 0 or of the other sign it would be
+// a NaN): a wave whose sums come out as NaN, as they do then, goes over its keys once more and takes
+// infinities and NaN out of the second products.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_decode.h"
 #include "kernels.h"
@@ -51,6 +55,17 @@ __device__ __forceinline__ Pair<bf16> split8(const float (&f)[8]) {
   for (int i = 0; i < 8; ++i) {
     h[i] = (bf16)f[i];
     l[i] = (bf16)(f[i] - (float)h[i]);
+  }
+  return {__builtin_bit_cast(uint4, h), __builtin_bit_cast(uint4, l)};
+}
+// the same of values that may be infinite: their first part alone
+__device__ __forceinline__ Pair<bf16> split8_any(const float (&f)[8]) {
+  bf16x8 h, l;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    h[i] = (bf16)f[i];
+    const float rest = f[i] - (float)h[i];
+    l[i] = (bf16)(__builtin_fabsf(rest) < INFINITY ? rest : 0.f);
   }
   return {__builtin_bit_cast(uint4, h), __builtin_bit_cast(uint4, l)};
 }
@@ -108,6 +123,26 @@ struct State {
   float m, l;
   f32x4 acc[G::EV];
 
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int j = 0; j < G::EV; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[j][r] = 0.f;
+  }
+  // Whether some lane's sum or value is a NaN (uniform).
+  __device__ __forceinline__ bool spoilt() const {
+    bool bad = l != l;
+#pragma unroll
+    for (int j = 0; j < G::EV; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) bad |= acc[j][r] != acc[j][r];
+    return __ballot(bad) != 0;
+  }
+
+  // GUARD: infinities and NaN of the cache enter the first products alone.
+  template <bool GUARD>
   __device__ __forceinline__ void add(const G &x, const Pair<T> (&q)[G::NS], int first, int n, int lane) {
     const int u = lane >> 4;
     f32x4 s[2];
@@ -119,7 +154,7 @@ struct State {
       for (int i = 0; i < G::NS; ++i) {
         if constexpr (sizeof(T) == 2) {
           s[t] = mfma16(as_bf16x8(x.k[t][i]), as_bf16x8(q[i].hi), s[t]);
-          s[t] = mfma16(as_bf16x8(x.k[t][i]), as_bf16x8(q[i].lo), s[t]);
+          s[t] = mfma16(as_bf16x8(GUARD ? part_of<T, Part::KEEP>(x.k[t][i]) : x.k[t][i]), as_bf16x8(q[i].lo), s[t]);
         } else {
           const uint4 &a = x.k[t][i], &b = q[i].hi;
           s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.x), __uint_as_float(b.x), s[t], 0, 0, 0);
@@ -165,9 +200,9 @@ struct State {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           w[i] = __builtin_amdgcn_perm(x.v[2 * i + 1][j / 2], x.v[2 * i][j / 2], (j & 1) ? 0x07060302u : 0x05040100u);
-        const bf16x8 a = as_bf16x8(make_uint4(w[0], w[1], w[2], w[3]));
-        acc[j] = mfma16(a, as_bf16x8(pb.hi), acc[j]);
-        acc[j] = mfma16(a, as_bf16x8(pb.lo), acc[j]);
+        const uint4 a = make_uint4(w[0], w[1], w[2], w[3]);
+        acc[j] = mfma16(as_bf16x8(a), as_bf16x8(pb.hi), acc[j]);
+        acc[j] = mfma16(as_bf16x8(GUARD ? part_of<T, Part::KEEP>(a) : a), as_bf16x8(pb.lo), acc[j]);
       }
     } else {
 #pragma unroll
@@ -222,7 +257,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void attn_decode_kernel(DecodeArgs 
 
   char *kc = a.kc.p + b * a.kc.batch + g * a.kc.head, *vc = a.vc.p + b * a.vc.batch + g * a.vc.head;
   GP x;
-  int row0 = first + wave * kGroup;
+  const int row0 = first + wave * kGroup;
   if (row0 < stop) x.fetch(kc, vc, a.kc.row, a.vc.row, row0, stop, a.hd, lane);
 
   // q and the new key, turned, in LDS; the new key and value into the cache
@@ -277,63 +312,68 @@ __global__ __launch_bounds__(kWaves * 64, 1) void attn_decode_kernel(DecodeArgs 
       float w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = f[i];
-      q[s] = split8(w);
+      q[s] = split8_any(w);
     } else {
       q[s].hi = *reinterpret_cast<const uint4 *>(f);
     }
   }
 
   State<T, DH> st;
-  st.m = -INFINITY;
-  st.l = 0.f;
-#pragma unroll
-  for (int j = 0; j < GP::EV; ++j)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) st.acc[j][r] = 0.f;
-
   // the next group is on the way while this one is used, where the registers hold both (fp32 rows
   // of 512 bytes: 128 registers a group; eight waves' loads keep the memory busy there)
   constexpr bool AHEAD = sizeof(T) * DH <= 256;
-  for (; row0 < stop; row0 += kWaves * kGroup) {
-    const int next = row0 + kWaves * kGroup;
-    if constexpr (AHEAD) {
-      GP y;
-      if (next < stop) y.fetch(kc, vc, a.kc.row, a.vc.row, next, stop, a.hd, lane);
-      st.add(x, q, row0, stop, lane);
-      if (next < stop) x = y;
-    } else {
-      st.add(x, q, row0, stop, lane);
-      if (next < stop) x.fetch(kc, vc, a.kc.row, a.vc.row, next, stop, a.hd, lane);
+  // The wave's keys, x holding its first group if it has any.
+  auto pass = [&](auto guard) {
+    constexpr bool GUARD = decltype(guard)::value;
+    st.clear();
+    for (int row = row0; row < stop; row += kWaves * kGroup) {
+      const int next = row + kWaves * kGroup;
+      if constexpr (AHEAD && !GUARD) {
+        GP y;
+        if (next < stop) y.fetch(kc, vc, a.kc.row, a.vc.row, next, stop, a.hd, lane);
+        st.template add<GUARD>(x, q, row, stop, lane);
+        if (next < stop) x = y;
+      } else {
+        st.template add<GUARD>(x, q, row, stop, lane);
+        if (next < stop) x.fetch(kc, vc, a.kc.row, a.vc.row, next, stop, a.hd, lane);
+      }
     }
-  }
-  if (split == 0 && wave == kWaves - 1) {  // the new token: a group of one key (its wave has the fewest others)
-    GP y;
+    if (split == 0 && wave == kWaves - 1) {  // the new token: a group of one key (its wave has the fewest others)
+      GP y;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int s = 0; s < GP::NS; ++s) {
-        y.k[t][s] = make_uint4(0, 0, 0, 0);
-        if (t == 0 && m16 == 0) {
-          const float *f = &qs[16][(4 * s + u4) * GP::E];
-          if constexpr (sizeof(T) == 2) {
-            float w[8];
+        for (int s = 0; s < GP::NS; ++s) {
+          y.k[t][s] = make_uint4(0, 0, 0, 0);
+          if (t == 0 && m16 == 0) {
+            const float *f = &qs[16][(4 * s + u4) * GP::E];
+            if constexpr (sizeof(T) == 2) {
+              float w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = f[i];
-            y.k[t][s] = split8(w).hi;
-          } else {
-            y.k[t][s] = *reinterpret_cast<const uint4 *>(f);
+              for (int i = 0; i < 8; ++i) w[i] = f[i];
+              y.k[t][s] = split8(w).hi;
+            } else {
+              y.k[t][s] = *reinterpret_cast<const uint4 *>(f);
+            }
           }
         }
-      }
-    const char *vs = a.v.p + b * a.v.batch + g * a.v.head;
+      const char *vs = a.v.p + b * a.v.batch + g * a.v.head;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int w = 0; w < GP::VW; ++w) {
-        const int at = m16 * GP::EV * (int)sizeof(T) + 4 * w;
-        y.v[i][w] = i == 0 && u4 == 0 && at < a.hd * (int)sizeof(T) ? *(const uint32_t *)(vs + at) : 0u;
-      }
-    st.add(y, q, 0, 1, lane);
+        for (int w = 0; w < GP::VW; ++w) {
+          const int at = m16 * GP::EV * (int)sizeof(T) + 4 * w;
+          y.v[i][w] = i == 0 && u4 == 0 && at < a.hd * (int)sizeof(T) ? *(const uint32_t *)(vs + at) : 0u;
+        }
+      st.template add<GUARD>(y, q, 0, 1, lane);
+    }
+  };
+  pass(std::false_type());
+  if constexpr (sizeof(T) == 2) {
+    if (__builtin_expect(st.spoilt(), 0)) {
+      if (row0 < stop) x.fetch(kc, vc, a.kc.row, a.vc.row, row0, stop, a.hd, lane);
+      pass(std::true_type());
+    }
   }
 
   // join the waves

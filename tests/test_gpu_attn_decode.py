@@ -162,3 +162,31 @@ def test_empty_batch():
     kc = torch.empty(0, 16, 4, 64, dtype=torch.bfloat16, device="cuda")
     n = torch.empty(0, dtype=torch.int32, device="cuda")
     assert dc.dynconv_attn_decode(q, q, q, kc, kc.clone(), n).shape == q.shape
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("S,n", [(1, 0), (40, 39), (40, 12), (700, 600), (5000, 4900)])
+@pytest.mark.parametrize("hd", [64, 96, 128])
+def test_seen_infinities(hd, S, n, dtype):
+    """Infinities and NaN in rows that are read, as in the sums themselves: a value of +infinity makes its
+    element +infinity; a key whose score is -infinity has no weight; a NaN, or +infinity and -infinity in one
+    element, makes that a NaN; a score of +infinity a head's whole row."""
+    _note(f"[decode] seen infinities {hd} {S} {n} {dtype}")
+    B, H, G = 2, 6, 2
+    q, k, v, kc, vc = (t.clone() for t in _inputs(B, S, H, G, hd, dtype, seed=S + hd))
+    q[:, :, 3] = q[:, :, 3].abs() + 0.25
+    q[:, :, 9] = -q[:, :, 9].abs() - 0.25
+    v[0, :, 0], v[0, 0, 1], v[1, 1, 2] = math.inf, -math.inf, math.nan
+    if n > 8:
+        vc[:, 4, 0, 5], vc[:, 7, 1, 6], vc[0, 2, :, 7], vc[0, 8, :, 7] = math.inf, -math.inf, math.inf, -math.inf
+        vc[1, 3, 1, 8] = math.nan
+        kc[:, 5, 0, 3], kc[:, 6, 1, 9], kc[:, 1, :, 3] = -math.inf, math.inf, -math.inf
+        k[1, :, 3] = -math.inf  # the new key of one sequence has no weight (and its NaN value no finite product)
+        v[1] = 1.0
+        q[1, 5, 4] = math.inf   # one head's scores are all infinite
+    lengths = torch.tensor([n, n], dtype=torch.int32, device="cuda")
+    ro, _, _ = au.decode(q, k, v, kc, vc, lengths)
+    o = dc.dynconv_attn_decode(q, k, v, kc, vc, lengths)
+    torch.cuda.synchronize()
+    assert au.rel(o, ro) <= TOL[dtype]
+    assert bool((o[0, :, 0] == math.inf).all())
