@@ -387,8 +387,8 @@ def _scale(scale) -> float:
     """The factor on q.k as the struct has it, where 0 stands for the default."""
     if scale is None:
         return 0.0
-    if 0.0 <= scale < 2.0 ** -126:
-        raise ValueError(f"scale must be positive and no less than 2^-126, got {scale}")
+    if 0.0 <= scale < 2.0 ** -120:
+        raise ValueError(f"scale must be positive and no less than 2^-120, got {scale}")
     return scale
 
 

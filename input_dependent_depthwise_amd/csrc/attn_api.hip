@@ -15,6 +15,10 @@ namespace {
 
 constexpr int64_t kMaxRow = 16 << 20;  // bytes between tokens: 64 rows stay below 2 GiB
 
+// The bf16 dk/dv kernel starts its sums at -lse / scale: the logarithm of up to 2^31 keys over this
+// is below 2^125 (at 2^-126 rows of 55 keys and more passed the largest float, and their p came out as 0).
+constexpr float kLeastScale = 0x1p-120f;
+
 struct Extent {  // what a view covers, in bytes
   const char *p;
   int64_t batch, row, head;  // strides, 0 for axes of length 1
@@ -103,7 +107,7 @@ int check_attn(const dynconv_attn *a, bool attention) {
   if (attention) {
     if (a->n_kv_heads <= 0 || a->n_heads % a->n_kv_heads != 0) return DYNCONV_E_SHAPE;
     if (a->head_dim % (a->dtype == DYNCONV_BF16 ? 8 : 4) != 0) return DYNCONV_E_SHAPE;
-    if (!(a->scale >= 0.f) || isinf(a->scale)) return DYNCONV_E_SHAPE;
+    if (!(a->scale == 0.f || a->scale >= kLeastScale) || isinf(a->scale)) return DYNCONV_E_SHAPE;
     if (a->head_dim > 128) return DYNCONV_E_LIMIT;
     // blocks of 256 threads, below 2^32 threads in all
     if (a->B > 0 && a->T > 0 && (a->T + 127) / 128 > (((int64_t)1 << 24) - 1) / a->n_heads / a->B) return DYNCONV_E_LIMIT;

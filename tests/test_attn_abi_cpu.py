@@ -224,3 +224,14 @@ def test_a_scale_of_zero_is_not_the_default():
     for s in (0, 0.0, 1e-39):
         with pytest.raises(ValueError):
             dc._scale(s)
+
+
+def test_scales_too_small_for_the_backward_are_refused(L):
+    """lse / scale would pass the largest float (the calls that need it have to agree on it)."""
+    small, least = attn(scale=2.0 ** -121), attn(scale=2.0 ** -120)
+    assert fwd(L, small) == SHAPE and bwd(L, small, nbytes=1 << 24) == SHAPE
+    assert decode(L, attn(T=1, scale=2.0 ** -126)) == SHAPE
+    assert L.dynconv_attn_bwd_workspace_bytes(ref(small)) == 0 < L.dynconv_attn_bwd_workspace_bytes(ref(least))
+    with pytest.raises(ValueError):
+        dc._scale(2.0 ** -121)
+    assert dc._scale(2.0 ** -120) == 2.0 ** -120

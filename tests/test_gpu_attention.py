@@ -383,3 +383,14 @@ def test_offsets_that_fall_stay_inside_the_row(cu, T, hd, dtype):
             assert bool((w[:, :room] == 7).all()) and bool((w[:, room + T:] == 7).all())
         seen.append([t.clone() for t in (o, lse, dq, dk, dv)])
     assert all(torch.equal(a, b) for a, b in zip(*seen))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_smallest_scale(dtype):
+    """At the smallest factor that a call takes all scores vanish: dv is the mean of do over the queries' keys."""
+    _note(f"[attn] smallest scale {dtype}")
+    q, k, v, d_o = _row(2, 300, 4, 2, 64, dtype, seed=23)
+    _compare(_run(q, k, v, d_o, scale=2.0 ** -120), au.attention(q, k, v, scale=2.0 ** -120, d_o=d_o), dtype)
+    for scale in (2.0 ** -121, 2.0 ** -126):
+        with pytest.raises(ValueError):
+            _run(q, k, v, d_o, scale=scale)
