@@ -394,3 +394,27 @@ def test_smallest_scale(dtype):
     for scale in (2.0 ** -121, 2.0 ** -126):
         with pytest.raises(ValueError):
             _run(q, k, v, d_o, scale=scale)
+
+
+def _off_over_own(got, ref, rows):
+    """The error over that of the definition rounded to bf16, both over the given [B, T] rows."""
+    got, ref = got.double()[rows], ref[rows]
+    return ((got - ref).norm() / (ref.bfloat16().double() - ref).norm()).item()
+
+
+@pytest.mark.parametrize("H,G,hd", [(8, 2, 64), (8, 2, 128), (9, 3, 96)])
+def test_few_keys_where_a_document_starts_before_a_block(H, G, hd):
+    """Rows of 2 to 8 keys at the head of a block of 128 queries, their document starting just before it.  Two
+    independent roundings to bf16 lie on the way to dq (ds and dq itself): 1.41 times dq's own; the rounding of o
+    in delta would make it 2.3."""
+    _note(f"[attn] documents across blocks {H} {G} {hd}")
+    T = 128 * 40
+    cu = [0] + [128 * m - 1 - m % 7 for m in range(1, 40)] + [T]
+    q, k, v, d_o = _row(1, T, H, G, hd, "bf16", seed=H + hd)
+    got, ref = _run(q, k, v, d_o, cu=cu), au.attention(q, k, v, cu=cu, d_o=d_o)
+    t, start = torch.arange(T, device="cuda"), torch.zeros(T, dtype=torch.int64, device="cuda")
+    for lo in cu[:-1]:
+        start[lo:] = lo
+    rows = ((t - start < 8) & (t - start > 0) & (t // 128 > start // 128))[None]
+    assert int(rows.sum()) > 100
+    assert _off_over_own(got["dq"], ref["dq"], rows) <= 1.7
