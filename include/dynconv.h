@@ -331,7 +331,8 @@ DYNCONV_API int dynconv_trace_next(int kernel, hipEvent_t start, hipEvent_t stop
  * on the matrix cores with fp32 sums; the softmax statistics, lse and delta =
  * do.o are fp32; with bf16 tensors p and ds are rounded to bf16 where they
  * enter a product, after their sum has been taken in fp32 (rows of up to 64
- * tokens keep 16 bits of them in the tiles on the diagonal).
+ * tokens, and packed documents of up to 64 where the row's T / n_seqs is no
+ * more than 64, keep 16 bits of them).
  *
  * A token of no sequence has no keys: its o and its gradients are zero and
  * its lse is -infinity.  What lies in masked places is never part of a

@@ -336,7 +336,7 @@ __device__ __forceinline__ void sum_rows(const unsigned char *t, int r0, const f
 }
 
 // acc += tile^T of what p loses when it is rounded to bf16 (KEPT: of the tile's finite values),
-// for the masked tiles of short rows: where few keys and queries meet, few roundings are
+// for short rows: where few keys and queries meet, few roundings are
 // averaged.  bf16, 3 tokens, error of dq and dk against 64 bits over that of their own rounding: 1.4
 // (1.7 at worst) without it, 1.0 with it; at 1000 tokens 1.4 (1.5) in any case without it.
 template <bool KEPT, typename T, int DH>
@@ -422,13 +422,16 @@ inline bool few_blocks(const AttnArgs &a) {
   return blocks <= kFewBlocks && blocks <= a.T / 2;
 }
 
-// Rows short enough to take sum_rows_rest.  Its products and registers cost 4096 rows of 16 tokens
-// (12 heads of 64) 363 -> 385 us forward and 1262 -> 1432 backward, one row of 37 nothing; they would
-// cost packed rows of 16384 (heads of 128) 5 % of the forward, of 8192 15 % of forward and
+// Rows, or packed documents on average, short enough to take sum_rows_rest in their masked tiles, and
+// in all of the few-block kernels' (whose tiles of 32 keys need no mask in rows of 33 tokens on; those of 64
+// are masked in any document of up to 64).  Its products and registers cost 4096 rows of 16 tokens
+// (12 heads of 64) 363 -> 385 us forward and 1262 -> 1432 backward, 8192 tokens in 256 documents 21 -> 25 us
+// forward and 130 -> 149 forward and backward (16 + 4 heads of 128: 44 -> 48, 255 -> 286), one row of 37 nothing; they
+// would cost packed rows of 16384 (heads of 128) 5 % of the forward, of 8192 15 % of forward and
 // backward, where the sums average the roundings.
 template <typename T>
 inline bool with_rest(const AttnArgs &a) {
-  return sizeof(T) == 2 && a.T <= 64;
+  return sizeof(T) == 2 && a.T <= 64 * (int64_t)(a.cu ? a.n_seqs : 1);
 }
 
 template <typename T, int DH>

@@ -153,7 +153,7 @@ struct Dq {
         sk.fetch(kh, krow, kt + 128, limit, hd, lane);
         sv.fetch(vh, vrow, kt + 128, limit, hd, lane);
       }
-      block<GUARD>(mine[0], mine[1], 0, kt, kt + 31 > qw || kt < w_full, met, lane);
+      block<GUARD>(mine[0], mine[1], 0, kt, REST || kt + 31 > qw || kt < w_full, met, lane);
       wave_sync();
       if (more) {
         sk.store(mine[0], lane);

@@ -52,7 +52,7 @@ struct Fwd {
   template <bool GUARD>
   __device__ __forceinline__ void step(const unsigned char *kl, const unsigned char *vl, int kt, bool &met, int lane) {
     const int h = lane >> 5;
-    const bool masked = kt + BN - 1 > qw || kt < w_full;
+    const bool masked = (REST && BN == 32) || kt + BN - 1 > qw || kt < w_full;
     f32x16 p[BN / 32];
 #pragma unroll
     for (int n = 0; n < BN / 32; ++n) {

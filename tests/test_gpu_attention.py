@@ -418,3 +418,30 @@ def test_few_keys_where_a_document_starts_before_a_block(H, G, hd):
     rows = ((t - start < 8) & (t - start > 0) & (t // 128 > start // 128))[None]
     assert int(rows.sum()) > 100
     assert _off_over_own(got["dq"], ref["dq"], rows) <= 1.7
+
+
+@pytest.mark.parametrize("hd", [64, 96, 128])
+@pytest.mark.parametrize("B,T", [(1, 33), (1, 60), (30, 60), (1, 64), (40, 64)])
+def test_rows_of_up_to_64_tokens_in_bf16_lose_no_more_than_their_own_rounding(B, T, hd):
+    """As above, with tiles that no mask cuts (keys 0 to 31 of queries 32 to 63)."""
+    _note(f"[attn] own rounding {B} {T} {hd}")
+    q, k, v, d_o = _row(B, T, 8, 4, hd, "bf16", seed=B + T + hd)
+    got, ref = _run(q, k, v, d_o), au.attention(q, k, v, d_o=d_o)
+    for n in ("o", "dq", "dk", "dv"):
+        off = (got[n].double() - ref[n]).norm()
+        own = (ref[n].bfloat16().double() - ref[n]).norm()
+        assert off <= 1.1 * own + 2.0 ** -16 * ref[n].norm(), (n, float(off / own))
+
+
+@pytest.mark.parametrize("hd", [64, 96, 128])
+@pytest.mark.parametrize("T,each,H", [(300, 3, 4), (600, 2, 4), (3900, 3, 9), (3910, 17, 9), (3968, 64, 9)])
+def test_packed_short_documents_in_bf16_lose_no_more_than_their_own_rounding(T, each, H, hd):
+    """The same documents as in rows of their own, behind one another in one row."""
+    _note(f"[attn] own rounding of documents of {each} in {T} {hd}")
+    cu = list(range(0, T + 1, each))
+    q, k, v, d_o = _row(1, T, H, H // 2 if H % 2 == 0 else 3, hd, "bf16", seed=T + hd)
+    got, ref = _run(q, k, v, d_o, cu=cu), au.attention(q, k, v, cu=cu, d_o=d_o)
+    for n in ("o", "dq", "dk", "dv"):
+        off = (got[n].double() - ref[n]).norm()
+        own = (ref[n].bfloat16().double() - ref[n]).norm()
+        assert off <= 1.1 * own + 2.0 ** -16 * ref[n].norm(), (n, float(off / own))
