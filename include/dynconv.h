@@ -404,7 +404,8 @@ DYNCONV_API int dynconv_rope_freqs(int rot_dim, double base, double stretch, dou
  * the last document's end).  y may be x's own view (in place); any other
  * overlap is refused.  Here head_dim and the strides may be any; a view of whole
  * 16-byte vectors with pairs that fill them takes the fast kernel.  More work than
- * 2^32 threads take in one launch is refused (DYNCONV_E_LIMIT).
+ * 2^32 threads take in one launch, or heads of 2 GiB and more to a token, is refused
+ * (DYNCONV_E_LIMIT).
  */
 DYNCONV_API int dynconv_rope(const dynconv_attn *a, const dynconv_rotary *r, const dynconv_view *x,
                              const int32_t *positions, const dynconv_view *y, hipStream_t stream);

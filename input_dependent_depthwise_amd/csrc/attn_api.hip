@@ -205,6 +205,8 @@ int dynconv_rope(const dynconv_attn *a, const dynconv_rotary *r, const dynconv_v
   if (positions && ((uintptr_t)positions & 3u) != 0) return DYNCONV_E_ALIGN;
   const int64_t lim = ((int64_t)1 << 31) - 4096;
   if (a->B > lim / a->T || a->B * a->T > lim * 256 / a->head_dim) return DYNCONV_E_LIMIT;
+  // the kernels count the vectors of a token and the bytes of a head in 32 bits
+  if (a->n_heads > lim / (a->head_dim * eb)) return DYNCONV_E_LIMIT;
   const bool in_place = ex.p == ey.p && ex.batch == ey.batch && ex.row == ey.row && ex.head == ey.head;
   if (!disjoint_rows(ey) || (!in_place && meet(ex, ey))) return DYNCONV_E_ALIAS;
   const Extent others[] = {flat(r->freqs, r->rot_dim / 2 * 8), flat(positions, positions ? a->B * a->T * 4 : 0),

@@ -235,3 +235,13 @@ def test_scales_too_small_for_the_backward_are_refused(L):
     with pytest.raises(ValueError):
         dc._scale(2.0 ** -121)
     assert dc._scale(2.0 ** -120) == 2.0 ** -120
+
+
+def test_rotary_tokens_past_2_gib_are_refused(L):
+    """Heads and widths whose product passes the kernels' 32-bit counts (65535 heads of 2^19 elements, bf16)."""
+    for heads, hd, dtype, want in ((65535, 1 << 19, dc.DYNCONV_BF16, LIMIT), (65535, 1 << 20, dc.DYNCONV_BF16, LIMIT),
+                                   (1, 1 << 30, dc.DYNCONV_BF16, LIMIT), (1, 1 << 29, dc.DYNCONV_FP32, LIMIT)):
+        x, y = View(addr(0), 0, 0, 0), View(1 << 45, 0, 0, hd)
+        for rot in (64, 4096):
+            a = attn(B=1, T=1, n_heads=heads, head_dim=hd, dtype=dtype)
+            assert rope(L, a, r=Rotary(rot, 0, 0, 1.0, 1 << 44), x=x, y=y) == want, (heads, hd, dtype, rot)
