@@ -21,6 +21,7 @@ import os
 import struct
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdynconv.so")
@@ -324,7 +325,7 @@ class DynConvFn(torch.autograd.Function):
     Pass W (head-wise, with n_heads) or A and U (low-rank), or none of them
     for the static filter (w0 alone; h may then be None); unused weights are
     None; cu_seqlens packs documents into one row.  The forward keeps the
-    fp32 generator cache for the backward.
+    fp32 generator cache for the backward.  First derivatives only.
     """
 
     @staticmethod
@@ -336,6 +337,7 @@ class DynConvFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         h, x, W, A, U, w0, cache, cu_seqlens = ctx.saved_tensors
         g = dynconv_bwd(h, x, dy.contiguous(), k=ctx.k, W=W, A=A, U=U, w0=w0, n_heads=ctx.n_heads,
@@ -563,7 +565,7 @@ class QKVAttnFn(torch.autograd.Function):
     row [B, T, (n_heads + 2 n_kv_heads) head_dim] (query, key and value heads
     side by side, as DynConvFn returns it) -> rotary positions on its query and
     key heads (freqs None: none) -> causal attention -> o [B, T, n_heads, head_dim].
-    The backward writes one gradient row, turned back in place.
+    The backward writes one gradient row, turned back in place.  First derivatives only.
     """
 
     @staticmethod
@@ -579,6 +581,7 @@ class QKVAttnFn(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_o):
         qk, v, o, lse, freqs, cu_seqlens = ctx.saved_tensors
         H, interleaved, factor, scale = ctx.args

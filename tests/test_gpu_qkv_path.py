@@ -112,3 +112,21 @@ def test_autograd_of_a_part_of_a_wider_row_and_a_broadcast_gradient():
     assert torch.equal(part.grad, plain.grad)
     with pytest.raises(ValueError):
         dc.QKVAttnFn.apply(plain, 2, 1, freqs, False, 1.0, 0.0)
+
+
+def test_second_derivatives_are_refused():
+    """The gradients carry no history of their own: differentiating them raises instead of leaving this part out."""
+    print("[path] second derivatives", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    freqs = dc.dynconv_rope_freqs(32, 10000.0)
+    row = torch.randn(1, 20, 4 * 32, generator=g, device="cuda").requires_grad_()
+    h, x = (torch.randn(1, 20, 32, generator=g, device="cuda").requires_grad_() for _ in range(2))
+    w0 = torch.randn(32, 4, generator=g, device="cuda").requires_grad_()
+    for part, leaves in ((dc.QKVAttnFn.apply(row, 2, 1, freqs), [row]),
+                         (dc.DynConvFn.apply(h, x, None, None, None, w0, 4, 0), [x, w0])):
+        # another part of the loss has a second derivative
+        loss = part.square().sum() + sum(t.pow(3).sum() for t in leaves)
+        first = torch.autograd.grad(loss, leaves, create_graph=True)
+        assert all(bool(torch.isfinite(t).all()) for t in first)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            sum(t.square().sum() for t in first).backward()
