@@ -21,6 +21,7 @@ import os
 import struct
 
 import torch
+from torch import _C
 from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -357,16 +358,22 @@ class DynConvFn(torch.autograd.Function):
 _VIEW, _ATTN, _ROTARY = struct.Struct("Pqqq").pack, struct.Struct("qqiiiifiPq").pack, struct.Struct("iiifP").pack
 
 
-def _pack_view(t: torch.Tensor, what: str, shape, dtype) -> bytes:
-    """The View of a [B, T, heads, head_dim] (or [B, heads, head_dim]) tensor of the given shape and dtype."""
+def _pack_view(t: torch.Tensor, what: str, shape, dtype, dev: int) -> bytes:
+    """The View of a [B, T, heads, head_dim] (or [B, heads, head_dim]) tensor of the given shape and dtype on GPU dev."""
     if t.shape != shape:
         raise ValueError(f"{what}: expected the shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{what}: expected a {dtype} tensor on the GPU, got {t.dtype} on {t.device}")
+    if t.get_device() != dev:
+        _other_device(t, what, dev)
     s = t.stride()
     if s[-1] != 1 and shape[-1] > 1 and t.numel():
         raise ValueError(f"{what}: the last axis must be contiguous, got strides {s}")
     return _VIEW(t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else _VIEW(t.data_ptr(), s[0], 0, s[1])
+
+
+def _other_device(t, what: str, dev: int):
+    raise ValueError(f"{what}: expected a tensor on cuda:{dev}, got one on {t.device}")
 
 
 def _dims(t: torch.Tensor, what: str, n: int):
@@ -375,13 +382,15 @@ def _dims(t: torch.Tensor, what: str, n: int):
     return t.shape
 
 
-def _int32(t, what: str, shape=None) -> int:
-    """Address of a contiguous int32 tensor on the GPU, 0 for None."""
+def _int32(t, what: str, dev: int, shape=None) -> int:
+    """Address of a contiguous int32 tensor on GPU dev, 0 for None."""
     if t is None:
         return 0
     if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or (shape is not None and t.shape != shape):
         raise TypeError(f"{what} must be a contiguous int32 tensor on the GPU"
                         + (f" of shape {tuple(shape)}" if shape is not None else ""))
+    if t.get_device() != dev:
+        _other_device(t, what, dev)
     return t.data_ptr()
 
 
@@ -394,36 +403,51 @@ def _scale(scale) -> float:
     return scale
 
 
-def _pack_attn(B, T, H, G, hd, dtype, scale, cu_seqlens) -> bytes:
+def _pack_attn(B, T, H, G, hd, dtype, dev, scale, cu_seqlens) -> bytes:
     if cu_seqlens is None:
         return _ATTN(B, T, H, G, hd, _dtype_code(dtype), _scale(scale), 0, 0, 0)
     if cu_seqlens.dim() != 1:
         raise TypeError("cu_seqlens must be a contiguous 1-d int32 tensor")
-    return _ATTN(B, T, H, G, hd, _dtype_code(dtype), _scale(scale), 0, _int32(cu_seqlens, "cu_seqlens"),
+    return _ATTN(B, T, H, G, hd, _dtype_code(dtype), _scale(scale), 0, _int32(cu_seqlens, "cu_seqlens", dev),
                  cu_seqlens.shape[0] - 1)
 
 
-def _pack_rotary(freqs: torch.Tensor, interleaved, inverse, factor) -> bytes:
+def _pack_rotary(freqs: torch.Tensor, interleaved, inverse, factor, dev) -> bytes:
     if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous() or not freqs.is_cuda:
         raise TypeError("freqs must be a contiguous 1-d float64 tensor on the GPU (radians per position, one per pair)")
+    if freqs.get_device() != dev:
+        _other_device(freqs, "freqs", dev)
     return _ROTARY(2 * freqs.shape[0], 1 if interleaved else 0, 1 if inverse else 0, factor, freqs.data_ptr())
 
 
-def _raw_stream(t: torch.Tensor) -> int:
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _launch(dev: int, where: str, call, *args) -> None:
+    """call(*args, stream) on the current stream of GPU dev, which is made the current device for it: that is where
+    a launch goes."""
+    if dev == _C._cuda_getDevice():
+        rc = call(*args, _C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = call(*args, _C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check(rc, where)
 
 
-def _on(stream, call, *args, **kw):
-    """call(...) with `stream` (a torch stream or a raw one) current, so that what it allocates belongs to that
-    stream too and is not handed out again while the stream still uses it."""
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
-    with torch.cuda.stream(s):
-        return call(*args, **kw)
+def _on(stream, call, t, *args, **kw):
+    """call(t, ...) with `stream` (a torch stream or a raw one of t's GPU) current, so that what it allocates belongs
+    to that stream too and is not handed out again while the stream still uses it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream: expected one of {t.device}, got one of {stream.device}")
+    with torch.cuda.stream(stream):
+        return call(t, *args, **kw)
 
 
-def _lse(lse, shape) -> int:
+def _lse(lse, shape, dev) -> int:
     if lse.dtype != torch.float32 or lse.shape != shape or not lse.is_contiguous() or not lse.is_cuda:
         raise TypeError(f"lse must be a contiguous float32 tensor {list(shape)} on the GPU")
+    if lse.get_device() != dev:
+        _other_device(lse, "lse", dev)
     return lse.data_ptr()
 
 
@@ -431,10 +455,10 @@ def _new(like: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
-def _out(t, like: torch.Tensor, what: str, shape, dtype):
+def _out(t, like: torch.Tensor, what: str, shape, dev: int):
     """An output and its View: the caller's, or a new contiguous one of like's shape."""
     if t is not None:
-        return t, _pack_view(t, what, shape, dtype)
+        return t, _pack_view(t, what, shape, like.dtype, dev)
     t = _new(like)
     row = shape[-2] * shape[-1]
     return t, _VIEW(t.data_ptr(), shape[1] * row if len(shape) == 4 else row, row, shape[-1])
@@ -464,14 +488,12 @@ def dynconv_rope(x, freqs, *, positions=None, cu_seqlens=None, interleaved=False
         return _on(stream, dynconv_rope, x, freqs, positions=positions, cu_seqlens=cu_seqlens, interleaved=interleaved,
                    factor=factor, inverse=inverse, out=out)
     B, T, H, hd = shape = _dims(x, "x", 4)
-    dt = x.dtype
-    a = _pack_attn(B, T, H, 1, hd, dt, None, cu_seqlens)
-    r = _pack_rotary(freqs, interleaved, inverse, factor)
-    vx = _pack_view(x, "x", shape, dt)
-    out, vy = _out(out, x, "out", shape, dt)
-    rc = lib().dynconv_rope(a, r, vx, _int32(positions, "positions", (B, T)), vy, _raw_stream(x))
-    if rc:
-        _check(rc, "dynconv_rope")
+    dt, dev = x.dtype, x.get_device()
+    vx = _pack_view(x, "x", shape, dt, dev)
+    a = _pack_attn(B, T, H, 1, hd, dt, dev, None, cu_seqlens)
+    r = _pack_rotary(freqs, interleaved, inverse, factor, dev)
+    out, vy = _out(out, x, "out", shape, dev)
+    _launch(dev, "dynconv_rope", lib().dynconv_rope, a, r, vx, _int32(positions, "positions", dev, (B, T)), vy)
     return out
 
 
@@ -483,21 +505,19 @@ def dynconv_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, o=None, lse=None, 
     if stream is not None:
         return _on(stream, dynconv_attn_fwd, q, k, v, scale=scale, cu_seqlens=cu_seqlens, o=o, lse=lse, want_lse=want_lse)
     B, T, H, hd = shape = _dims(q, "q", 4)
-    G, dt = _dims(k, "k", 4)[2], q.dtype
+    G, dt, dev = _dims(k, "k", 4)[2], q.dtype, q.get_device()
     kv = (B, T, G, hd)
-    a, vq = _pack_attn(B, T, H, G, hd, dt, scale, cu_seqlens), _pack_view(q, "q", shape, dt)
-    o, vo = _out(o, q, "o", shape, dt)
+    vq, a = _pack_view(q, "q", shape, dt, dev), _pack_attn(B, T, H, G, hd, dt, dev, scale, cu_seqlens)
+    o, vo = _out(o, q, "o", shape, dev)
     if lse is not None:
-        pl = _lse(lse, (B, H, T))
+        pl = _lse(lse, (B, H, T), dev)
     elif want_lse:
         lse = q.new_empty((B, H, T), dtype=torch.float32)
         pl = lse.data_ptr()
     else:
         pl = None
-    rc = lib().dynconv_attn_fwd(a, vq, _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt), vo, pl,
-                                _raw_stream(q))
-    if rc:
-        _check(rc, "dynconv_attn_fwd")
+    _launch(dev, "dynconv_attn_fwd", lib().dynconv_attn_fwd, a, vq, _pack_view(k, "k", kv, dt, dev),
+            _pack_view(v, "v", kv, dt, dev), vo, pl)
     return (o, lse) if want_lse else o
 
 
@@ -509,22 +529,20 @@ def dynconv_attn_bwd(q, k, v, o, lse, d_o, *, scale=None, cu_seqlens=None, out=N
         return _on(stream, dynconv_attn_bwd, q, k, v, o, lse, d_o, scale=scale, cu_seqlens=cu_seqlens, out=out,
                    workspace=workspace)
     B, T, H, hd = shape = _dims(q, "q", 4)
-    G, dt = _dims(k, "k", 4)[2], q.dtype
+    G, dt, dev = _dims(k, "k", 4)[2], q.dtype, q.get_device()
     kv = (B, T, G, hd)
-    a = _pack_attn(B, T, H, G, hd, dt, scale, cu_seqlens)
-    ins = (_pack_view(q, "q", shape, dt), _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt),
-           _pack_view(o, "o", shape, dt), _lse(lse, (B, H, T)), _pack_view(d_o, "d_o", shape, dt))
+    ins = (_pack_view(q, "q", shape, dt, dev), _pack_view(k, "k", kv, dt, dev), _pack_view(v, "v", kv, dt, dev),
+           _pack_view(o, "o", shape, dt, dev), _lse(lse, (B, H, T), dev), _pack_view(d_o, "d_o", shape, dt, dev))
+    a = _pack_attn(B, T, H, G, hd, dt, dev, scale, cu_seqlens)
     out = out or {}
-    dq, vdq = _out(out.get("dq"), q, "dq", shape, dt)
-    dk, vdk = _out(out.get("dk"), k, "dk", kv, dt)
-    dv, vdv = _out(out.get("dv"), v, "dv", kv, dt)
+    dq, vdq = _out(out.get("dq"), q, "dq", shape, dev)
+    dk, vdk = _out(out.get("dk"), k, "dk", kv, dev)
+    dv, vdv = _out(out.get("dv"), v, "dv", kv, dev)
     L = lib()
     ws = workspace
     if ws is None:
         ws = q.new_empty(L.dynconv_attn_bwd_workspace_bytes(a) or 1, dtype=torch.uint8)
-    rc = L.dynconv_attn_bwd(a, *ins, vdq, vdk, vdv, ws.data_ptr(), ws.nbytes, _raw_stream(q))
-    if rc:
-        _check(rc, "dynconv_attn_bwd")
+    _launch(dev, "dynconv_attn_bwd", L.dynconv_attn_bwd, a, *ins, vdq, vdk, vdv, ws.data_ptr(), ws.nbytes)
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
@@ -540,21 +558,20 @@ def dynconv_attn_decode(q, k, v, k_cache, v_cache, lengths, *, scale=None, freqs
         return _on(stream, dynconv_attn_decode, q, k, v, k_cache, v_cache, lengths, scale=scale, freqs=freqs,
                    interleaved=interleaved, factor=factor, o=o, workspace=workspace)
     B, H, hd = shape = _dims(q, "q", 3)
-    G, dt, cap = _dims(k, "k", 3)[1], q.dtype, _dims(k_cache, "k_cache", 4)[1]
+    G, cap = _dims(k, "k", 3)[1], _dims(k_cache, "k_cache", 4)[1]
+    dt, dev = q.dtype, q.get_device()
     kv, rows = (B, G, hd), (B, cap, G, hd)
-    a = _pack_attn(B, 1, H, G, hd, dt, scale, None)
-    vq = _pack_view(q, "q", shape, dt)
-    o, vo = _out(o, q, "o", shape, dt)
+    vq = _pack_view(q, "q", shape, dt, dev)
+    a = _pack_attn(B, 1, H, G, hd, dt, dev, scale, None)
+    o, vo = _out(o, q, "o", shape, dev)
     L = lib()
     nbytes = L.dynconv_attn_decode_workspace_bytes(a, cap)
     ws = _workspace(nbytes, q.device, workspace) if nbytes else None
-    rc = L.dynconv_attn_decode(
-        a, None if freqs is None else _pack_rotary(freqs, interleaved, False, factor), vq,
-        _pack_view(k, "k", kv, dt), _pack_view(v, "v", kv, dt), _pack_view(k_cache, "k_cache", rows, dt),
-        _pack_view(v_cache, "v_cache", rows, dt), cap, _int32(lengths, "lengths", (B,)), vo, _ptr(ws),
-        0 if ws is None else ws.nbytes, _raw_stream(q))
-    if rc:
-        _check(rc, "dynconv_attn_decode")
+    _launch(dev, "dynconv_attn_decode", L.dynconv_attn_decode, a,
+            None if freqs is None else _pack_rotary(freqs, interleaved, False, factor, dev), vq,
+            _pack_view(k, "k", kv, dt, dev), _pack_view(v, "v", kv, dt, dev),
+            _pack_view(k_cache, "k_cache", rows, dt, dev), _pack_view(v_cache, "v_cache", rows, dt, dev), cap,
+            _int32(lengths, "lengths", dev, (B,)), vo, _ptr(ws), 0 if ws is None else ws.nbytes)
     return o
 
 

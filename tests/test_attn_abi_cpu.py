@@ -245,3 +245,79 @@ def test_rotary_tokens_past_2_gib_are_refused(L):
         for rot in (64, 4096):
             a = attn(B=1, T=1, n_heads=heads, head_dim=hd, dtype=dtype)
             assert rope(L, a, r=Rotary(rot, 0, 0, 1.0, 1 << 44), x=x, y=y) == want, (heads, hd, dtype, rot)
+
+
+class OnGPU:
+    """What the binding asks of a tensor, on a GPU of the given index."""
+    is_cuda = True
+
+    def __init__(self, index, shape=(1, 4, 2, 64), dtype=None):
+        import torch
+        self.index, self.shape = index, torch.Size(shape)
+        self.dtype, self.device = dtype or torch.bfloat16, torch.device("cuda", index)
+
+    def get_device(self):
+        return self.index
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return tuple(math.prod(self.shape[i + 1:]) for i in range(len(self.shape)))
+
+    def data_ptr(self):
+        return addr(self.index)
+
+    def numel(self):
+        return math.prod(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+
+def test_launches_go_to_the_tensors_gpu(monkeypatch):
+    """A launch goes to the current device: it is the tensors' for the time of the call, with its own current stream."""
+    import contextlib
+
+    import torch
+    seen, current = [], [0]
+
+    @contextlib.contextmanager
+    def device(index):
+        before, current[0] = current[0], index
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 1000 + i, raising=False)
+
+    class Lib:
+        def dynconv_rope(self, *args):
+            seen.append((current[0], args[-1]))
+            return 0
+
+        dynconv_attn_fwd = dynconv_rope
+
+    monkeypatch.setattr(dc, "lib", Lib)
+    for index in (0, 1, 0):
+        x = OnGPU(index)
+        dc.dynconv_rope(x, OnGPU(index, (32,), torch.float64), out=x)
+    assert seen == [(0, 1000), (1, 1001), (0, 1000)] and current == [0]
+    # tensors of several GPUs, and a stream of another one
+    x = OnGPU(1)
+    for kw in (dict(freqs=OnGPU(0, (32,), torch.float64)), dict(out=OnGPU(0)), dict(positions=OnGPU(0, (1, 4), torch.int32)),
+               dict(cu_seqlens=OnGPU(0, (2,), torch.int32))):
+        with pytest.raises(ValueError, match="cuda:1"):
+            dc.dynconv_rope(x, **{"freqs": OnGPU(1, (32,), torch.float64), "out": x, **kw})
+    for q, k, v in ((x, OnGPU(0), x), (x, x, OnGPU(0))):
+        with pytest.raises(ValueError, match="cuda:1"):
+            dc.dynconv_attn_fwd(q, k, v, o=OnGPU(1))
+
+    class Stream:
+        device = torch.device("cuda", 0)
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    with pytest.raises(ValueError, match="cuda:1"):
+        dc.dynconv_rope(x, OnGPU(1, (32,), torch.float64), out=x, stream=Stream())
+    assert len(seen) == 3
