@@ -213,6 +213,8 @@ def dynconv_gen_cache_bytes(prob: Problem, gen: Gen) -> int:
 
 def _workspace(nbytes: int, device, workspace):
     if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise TypeError(f"workspace must be a contiguous tensor on {device}, got one on {workspace.device}")
         return workspace
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 
@@ -539,9 +541,7 @@ def dynconv_attn_bwd(q, k, v, o, lse, d_o, *, scale=None, cu_seqlens=None, out=N
     dk, vdk = _out(out.get("dk"), k, "dk", kv, dev)
     dv, vdv = _out(out.get("dv"), v, "dv", kv, dev)
     L = lib()
-    ws = workspace
-    if ws is None:
-        ws = q.new_empty(L.dynconv_attn_bwd_workspace_bytes(a) or 1, dtype=torch.uint8)
+    ws = _workspace(L.dynconv_attn_bwd_workspace_bytes(a), q.device, workspace)
     _launch(dev, "dynconv_attn_bwd", L.dynconv_attn_bwd, a, *ins, vdq, vdk, vdv, ws.data_ptr(), ws.nbytes)
     return {"dq": dq, "dk": dk, "dv": dv}
 
@@ -566,7 +566,7 @@ def dynconv_attn_decode(q, k, v, k_cache, v_cache, lengths, *, scale=None, freqs
     o, vo = _out(o, q, "o", shape, dev)
     L = lib()
     nbytes = L.dynconv_attn_decode_workspace_bytes(a, cap)
-    ws = _workspace(nbytes, q.device, workspace) if nbytes else None
+    ws = _workspace(nbytes, q.device, workspace) if nbytes or workspace is not None else None
     _launch(dev, "dynconv_attn_decode", L.dynconv_attn_decode, a,
             None if freqs is None else _pack_rotary(freqs, interleaved, False, factor, dev), vq,
             _pack_view(k, "k", kv, dt, dev), _pack_view(v, "v", kv, dt, dev),

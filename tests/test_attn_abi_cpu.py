@@ -321,3 +321,17 @@ def test_launches_go_to_the_tensors_gpu(monkeypatch):
     with pytest.raises(ValueError, match="cuda:1"):
         dc.dynconv_rope(x, OnGPU(1, (32,), torch.float64), out=x, stream=Stream())
     assert len(seen) == 3
+
+
+def test_a_workspace_of_the_callers_is_checked():
+    import torch
+    dev = torch.device("cuda", 0)
+    host, meta = torch.empty(64, dtype=torch.uint8), torch.empty(64, dtype=torch.uint8, device="meta")
+    for bad in (host, meta):
+        with pytest.raises(TypeError, match="workspace"):
+            dc._workspace(16, dev, bad)
+    with pytest.raises(TypeError, match="workspace"):
+        dc._workspace(16, host.device, host[::2])  # every other byte of a buffer that is not all the caller's
+    assert dc._workspace(16, host.device, host) is host
+    with pytest.raises(TypeError, match="workspace"):
+        dc._workspace(16, OnGPU(1).device, OnGPU(0, (64,), torch.uint8))

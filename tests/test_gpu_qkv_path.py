@@ -130,3 +130,22 @@ def test_second_derivatives_are_refused():
         assert all(bool(torch.isfinite(t).all()) for t in first)
         with pytest.raises(RuntimeError, match="once_differentiable"):
             sum(t.square().sum() for t in first).backward()
+
+
+def test_a_workspace_of_the_callers():
+    """One that is on the GPU and whole is used, others are refused before the call."""
+    print("[path] workspace", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q, k, v, d_o = (torch.randn(1, 300, 2, 64, generator=g, device="cuda").bfloat16() for _ in range(4))
+    o, lse = dc.dynconv_attn_fwd(q, k, v, want_lse=True)
+    want = dc.dynconv_attn_bwd(q, k, v, o, lse, d_o)
+    room = torch.empty(1 << 20, device="cuda")
+    got = dc.dynconv_attn_bwd(q, k, v, o, lse, d_o, workspace=room)
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    cache = torch.zeros(1, 4000, 2, 64, dtype=torch.bfloat16, device="cuda")
+    n = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for bad in (torch.empty(1 << 20), room[::2]):
+        with pytest.raises(TypeError, match="workspace"):
+            dc.dynconv_attn_bwd(q, k, v, o, lse, d_o, workspace=bad)
+        with pytest.raises(TypeError, match="workspace"):
+            dc.dynconv_attn_decode(q[:, 0], k[:, 0], v[:, 0], cache, cache.clone(), n, workspace=bad)
