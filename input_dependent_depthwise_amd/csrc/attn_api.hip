@@ -69,27 +69,26 @@ bool disjoint_rows(const Extent &x) {
   return true;
 }
 
-// Whether two views might share an element.  Views that interleave in one buffer
-// (heads of one row, or rows of one batch) are told apart where both repeat with
-// the same period and each stays within it.
+// Whether two views might share an element.  Views that interleave in one buffer (heads of one row, rows of
+// one batch, on whatever axis they alternate) are told apart by a stride of one of them as a period: strides that
+// are multiples of it do not matter then, and what the others cover of each view has to lie beside the
+// other's within the period.
 bool meet(const Extent &a, const Extent &b) {
   const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
   if (a0 + (uint64_t)a.span <= b0 || b0 + (uint64_t)b.span <= a0) return false;
   const int64_t d = (int64_t)(b0 - a0);
-  auto apart = [&](int64_t period, int64_t fa, int64_t fb) {
-    if (period <= 0 || fa > period || fb > period) return false;
-    const int64_t m = ((d % period) + period) % period;
-    return m >= fa && m + fb <= period;
+  auto cover = [](const Extent &x, int64_t period) {  // bytes from its first element on, modulo the period
+    const int64_t s[3] = {x.batch, x.row, x.head}, n[3] = {x.B, x.T, x.H};
+    int64_t c = x.len;
+    for (int i = 0; i < 3; ++i)
+      if (n[i] > 1 && s[i] % period != 0) c += (n[i] - 1) * s[i];
+    return c;
   };
-  const int64_t ha = (a.H - 1) * a.head + a.len, hb = (b.H - 1) * b.head + b.len;
-  auto steps = [](const Extent &x, int64_t row) {  // its rows lie at multiples of `row`
-    return (x.T <= 1 || x.row == row) && (x.B <= 1 || x.batch % row == 0);
-  };
-  const int64_t row = a.row ? a.row : b.row, batch = a.batch ? a.batch : b.batch;
-  if (row > 0 && steps(a, row) && steps(b, row) && apart(row, ha, hb)) return false;
-  if (batch > 0 && (a.B <= 1 || a.batch == batch) && (b.B <= 1 || b.batch == batch) &&
-      apart(batch, ha + (a.T - 1) * a.row, hb + (b.T - 1) * b.row))
-    return false;
+  for (int64_t period : {a.batch, a.row, a.head, b.batch, b.row, b.head}) {
+    if (period <= 0) continue;
+    const int64_t ca = cover(a, period), cb = cover(b, period), m = ((d % period) + period) % period;
+    if (m >= ca && m + cb <= period) return false;
+  }
   return true;
 }
 

@@ -335,3 +335,77 @@ def test_a_workspace_of_the_callers_is_checked():
     assert dc._workspace(16, host.device, host) is host
     with pytest.raises(TypeError, match="workspace"):
         dc._workspace(16, OnGPU(1).device, OnGPU(0, (64,), torch.uint8))
+
+
+@pytest.fixture
+def no_gpu():
+    """For calls whose checks pass: they go on to the launch, which fails without a GPU (the addresses are made up)."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("would launch on made-up addresses")
+
+
+def test_views_that_interleave_pass(L, no_gpu):
+    """Parts of one buffer that share no element, whichever axis they alternate on: none of them is an overlap."""
+    B, T, H, G, hd = 2, 100, 8, 2, 64
+    e, N = 2, H + 2 * G
+
+    def bwd_into(dq, dk, dv):
+        a = attn()
+        return L.dynconv_attn_bwd(ref(a), ref(view(0, 8)), ref(view(1, 2)), ref(view(2, 2)), ref(view(3, 8)), addr(9),
+                                  ref(view(4, 8)), ref(dq), ref(dk), ref(dv), addr(15), 1 << 24, None)
+
+    def at(first, batch, row, head):
+        return View(addr(5) + first * e, batch, row, head)
+
+    row = N * hd
+    good = {
+        "parts of a row": [at(f * hd, T * row, row, hd) for f in (0, H, H + G)],
+        "parts of a token, tokens outside": [at(f * hd, row, B * row, hd) for f in (0, H, H + G)],
+        "head-major parts of a batch row": [at(f * T * hd, N * T * hd, hd, T * hd) for f in (0, H, H + G)],
+        "head-major parts, batches inside": [at(f * T * B * hd, T * hd, hd, B * T * hd) for f in (0, H, H + G)],
+    }
+    for name, views in good.items():
+        assert bwd_into(*views) != ALIAS, name
+    # a group's key between its queries and its value: [B, T, G, n + 2, hd] with one query head to a group
+    one = attn(n_heads=2, n_kv_heads=2)
+    group = [at(i * hd, T * 2 * 3 * hd, 2 * 3 * hd, 3 * hd) for i in range(3)]
+    ins = [ref(view(i, 2)) for i in range(5)]
+    assert L.dynconv_attn_bwd(ref(one), *ins[:4], addr(9), ins[4], *[ref(v) for v in group], addr(15), 1 << 24, None) != ALIAS
+    for i in range(3):  # one element further to the left or right is in the neighbour's head
+        for by in (-8, 8):
+            moved = list(group)
+            moved[i] = View(group[i].data + by * e, group[i].batch, group[i].row, group[i].head)
+            assert L.dynconv_attn_bwd(ref(one), *ins[:4], addr(9), ins[4], *[ref(v) for v in moved], addr(15), 1 << 24,
+                                      None) == ALIAS
+    assert bwd_into(at(0, T * row, row, hd), at((H - 1) * hd, T * row, row, hd), at((H + G) * hd, T * row, row, hd)) == ALIAS
+    assert bwd_into(at(0, row, B * row, hd), at(H * hd, row, B * row, hd), at((H + G + 1) * hd, row, B * row, hd)) == ALIAS
+
+
+def test_overlaps_are_found(L, no_gpu):
+    """Small views of one buffer with drawn strides: whatever shares an element is refused."""
+    import itertools
+    import random
+    r = random.Random(3)
+    B, T, H, hd, e = 2, 3, 2, 8, 2
+    a = attn(B=B, T=T, n_heads=H, n_kv_heads=H, head_dim=hd)
+    far = [ref(View(addr(i), T * H * hd, H * hd, hd)) for i in range(2)]
+
+    def elements(v):
+        return {(v.data - addr(5)) // e + b * v.batch + t * v.row + h * v.head + i
+                for b, t, h, i in itertools.product(range(B), range(T), range(H), range(hd))}
+
+    def drawn():
+        s = r.choice(list(itertools.permutations((1, 2, 3, 4, 6, 8, 12), 3)) + [(6, 2, 1), (12, 4, 2), (12, 4, 1), (2, 4, 1)])
+        return View(addr(5) + 16 * r.randrange(12), *(8 * x for x in s))
+
+    refused = passed = 0
+    for i in range(4000):
+        v, o = drawn(), drawn()
+        if i % 2:  # the same strides, another place
+            o = View(o.data, v.batch, v.row, v.head)
+        rc = L.dynconv_attn_fwd(ref(a), *far, ref(v), ref(o), None, None)
+        shared = bool(elements(v) & elements(o)) or len(elements(o)) < B * T * H * hd
+        assert rc == ALIAS or not shared, (v.data, v.batch, v.row, v.head, o.data, o.batch, o.row, o.head)
+        refused, passed = refused + (rc == ALIAS), passed + (rc != ALIAS)
+    assert refused > 100 and passed > 100

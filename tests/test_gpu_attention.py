@@ -445,3 +445,29 @@ def test_packed_short_documents_in_bf16_lose_no_more_than_their_own_rounding(T, 
         off = (got[n].double() - ref[n]).norm()
         own = (ref[n].bfloat16().double() - ref[n]).norm()
         assert off <= 1.1 * own + 2.0 ** -16 * ref[n].norm(), (n, float(off / own))
+
+
+def test_gradients_into_parts_of_one_buffer():
+    """dq, dk and dv side by side in one buffer on any axis, tokens outside the batch or a group's heads together:
+    bitwise as in tensors of their own."""
+    _note("[attn] parts of one buffer")
+    B, T, H, G, hd = 2, 150, 4, 2, 64
+    q, k, v, d_o = _row(B, T, H, G, hd, "bf16", seed=29)
+    o, lse = dc.dynconv_attn_fwd(q, k, v, want_lse=True)
+    want = dc.dynconv_attn_bwd(q, k, v, o, lse, d_o)
+    new = lambda *shape: torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    tokens_outside = new(T, B, H + 2 * G, hd).transpose(0, 1)
+    head_major = new(B, H + 2 * G, T, hd).transpose(1, 2)
+    for row in (tokens_outside, head_major):
+        out = {"dq": row[:, :, :H], "dk": row[:, :, H:H + G], "dv": row[:, :, H + G:]}
+        dc.dynconv_attn_bwd(q, k, v, o, lse, d_o, out=out)
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[n], want[n]) for n in want)
+    groups = new(B, T, G, 3, hd)
+    one = q[:, :, :G]
+    o, lse = dc.dynconv_attn_fwd(one, k, v, want_lse=True)
+    want = dc.dynconv_attn_bwd(one, k, v, o, lse, d_o[:, :, :G])
+    out = {n: groups[:, :, :, i] for i, n in enumerate(("dq", "dk", "dv"))}
+    dc.dynconv_attn_bwd(one, k, v, o, lse, d_o[:, :, :G], out=out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out[n], want[n]) for n in want)
