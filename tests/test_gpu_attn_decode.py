@@ -190,3 +190,28 @@ def test_seen_infinities(hd, S, n, dtype):
     torch.cuda.synchronize()
     assert au.rel(o, ro) <= TOL[dtype]
     assert bool((o[0, :, 0] == math.inf).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape,lengths", [((3, 40, 4, 2, 64), [31, 0, -1]), ((2, 3000, 6, 2, 96), [2500, 3000]),
+                                           ((1, 5000, 8, 1, 128), [4097])], ids=["40", "3000", "5000"])
+def test_no_other_cache_row_is_written(shape, lengths, dtype):
+    """Bit for bit, NaN of every payload among them (a zero written over a NaN would show)."""
+    _note(f"[decode] other rows {shape} {lengths} {dtype}")
+    B, S, H, G, hd = shape
+    q, k, v, kc, vc = _inputs(*shape, dtype, seed=S)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    g = torch.Generator(device="cuda").manual_seed(S)
+    for c in (kc, vc):
+        for b, n in enumerate(lengths):
+            if n >= 0:  # rows that are not read hold any bits
+                c[b, n:].view(bits).random_(generator=g)
+    before = kc.view(bits).clone(), vc.view(bits).clone()
+    dc.dynconv_attn_decode(q, k, v, kc, vc, torch.tensor(lengths, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    for c, old, new in ((kc, before[0], k), (vc, before[1], v)):
+        want = old.clone()
+        for b, n in enumerate(lengths):
+            if 0 <= n < S:
+                want[b, n] = new.view(bits)[b]
+        assert torch.equal(c.view(bits), want)
