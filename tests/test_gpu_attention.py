@@ -471,3 +471,16 @@ def test_gradients_into_parts_of_one_buffer():
     dc.dynconv_attn_bwd(one, k, v, o, lse, d_o[:, :, :G], out=out)
     torch.cuda.synchronize()
     assert all(torch.equal(out[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("B,T,H,G,hd", [(2, 129, 4, 2, 64), (1, 515, 12, 12, 64), (1, 1030, 16, 4, 128), (2, 257, 4, 1, 80),
+                                        (16, 260, 8, 2, 128), (2, 2100, 8, 4, 64)])
+def test_longer_rows_in_bf16_add_one_rounding_to_their_own(B, T, H, G, hd):
+    """p or ds rounded once and the output rounded once, independent of each other and of like size: 1.41 times
+    the output's own.  A product that lost one more bit would be at 2.2."""
+    _note(f"[attn] one rounding more {B} {T} {H} {G} {hd}")
+    q, k, v, d_o = _row(B, T, H, G, hd, "bf16", seed=T + hd)
+    got, ref = _run(q, k, v, d_o), au.attention(q, k, v, d_o=d_o)
+    every = torch.ones(B, T, dtype=torch.bool, device="cuda")
+    errs = {n: _off_over_own(got[n], ref[n], every) for n in ("o", "dq", "dk", "dv")}
+    assert all(e <= 1.75 for e in errs.values()), errs
