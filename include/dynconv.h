@@ -335,7 +335,8 @@ DYNCONV_API int dynconv_trace_next(int kernel, hipEvent_t start, hipEvent_t stop
  * more than 64, keep 16 bits of them).
  *
  * A token of no sequence has no keys: its o and its gradients are zero and
- * its lse is -infinity.  What lies in masked places is never part of a
+ * its lse is -infinity; o and lse of a token whose scores are all -infinity
+ * are the same.  What lies in masked places is never part of a
  * result, infinities and NaN included: a later token, another document or
  * the padding cannot reach a row that does not see it.
  */

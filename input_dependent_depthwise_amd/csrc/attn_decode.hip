@@ -46,6 +46,9 @@ __device__ __forceinline__ int active_splits(int n, int n_split) {
   return max(1, (ng + per - 1) / per);
 }
 
+// o from the joined sums (t = 0: every score was -infinity, no key has a weight)
+__device__ __forceinline__ float quotient(float s, float t) { return t == 0.f ? 0.f : s / t; }
+
 template <typename T> struct Pair { uint4 hi, lo; };  // a B operand as hi + lo (fp32: hi alone)
 
 // bf16 rounding of 8 values and of what it left
@@ -404,7 +407,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void attn_decode_kernel(DecodeArgs 
       t = __builtin_fmaf(f, tots[w][col], t);
     }
     if (a.n_split == 1) {
-      *(T *)(a.o.p + b * a.o.batch + (e0 + col) * a.o.head + d * sizeof(T)) = from_f32<T>(s / t);
+      *(T *)(a.o.p + b * a.o.batch + (e0 + col) * a.o.head + d * sizeof(T)) = from_f32<T>(quotient(s, t));
     } else {
       const int64_t at = ((int64_t)b * a.H + e0 + col) * a.n_split + split;
       a.part[at * a.hd + d] = s;
@@ -434,7 +437,7 @@ __global__ __launch_bounds__(128) void attn_decode_join_kernel(DecodeArgs a) {
     s = __builtin_fmaf(f, a.part[(at + i) * a.hd + d], s);
     t = __builtin_fmaf(f, ml[2 * i + 1], t);
   }
-  *(T *)(a.o.p + b * a.o.batch + e * a.o.head + d * sizeof(T)) = from_f32<T>(s / t);
+  *(T *)(a.o.p + b * a.o.batch + e * a.o.head + d * sizeof(T)) = from_f32<T>(quotient(s, t));
 }
 
 template <typename T>

@@ -215,3 +215,22 @@ def test_no_other_cache_row_is_written(shape, lengths, dtype):
             if 0 <= n < S:
                 want[b, n] = new.view(bits)[b]
         assert torch.equal(c.view(bits), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("S,n", [(1, 0), (60, 40), (5000, 4000)])
+def test_scores_that_are_all_minus_infinity(S, n, dtype):
+    """A row without any weight is zero, as in the whole-sequence call; the other heads keep theirs."""
+    _note(f"[decode] all -infinity {S} {n} {dtype}")
+    H, G, hd = 4, 2, 64
+    q, k, v, kc, vc = (t.clone() for t in _inputs(1, S, H, G, hd, dtype, seed=S))
+    q[:, :2, 3] = 1.0
+    k[:, 0, 3], kc[:, :, 0, 3] = -math.inf, -math.inf
+    keys, values = torch.cat((kc[:, :n], k[:, None]), 1), torch.cat((vc[:, :n], v[:, None]), 1)
+    o = dc.dynconv_attn_decode(q, k, v, kc, vc, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    rows = q[:, None].expand(-1, n + 1, -1, -1).contiguous()
+    want, lse = dc.dynconv_attn_fwd(rows, keys, values, want_lse=True)
+    torch.cuda.synchronize()
+    assert bool((want[:, -1, :2] == 0).all()) and bool((lse[:, :2] == -math.inf).all())
+    assert bool((o[:, :2] == 0).all())
+    assert au.rel(o[:, 2:], want[:, -1, 2:].double()) <= (4 * 2.0 ** -8 if dtype == "bf16" else 1e-5)
