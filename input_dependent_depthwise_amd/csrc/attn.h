@@ -1,6 +1,6 @@
 // attn.h -- internal pieces of libdynconv's attention kernels: arguments,
 // document bounds, LDS tiles and matrix-core fragments (attn_fwd.hip,
-// attn_bwd.hip).
+// attn_bwd.h).
 //
 // All three attention kernels have the same form.  A wave owns 32 rows (the
 // queries in the forward and in dq, the keys in dk/dv), one per lane column;
@@ -231,19 +231,6 @@ __device__ __forceinline__ void read_ahead() {
     __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
   }
   __builtin_amdgcn_sched_group_barrier(0x008, MFMAS * AHEAD, 0);
-}
-
-// The same with VALU other vector operations after each product.
-template <int N, int READS, int AHEAD, int VALU>
-__device__ __forceinline__ void beside() {
-  __builtin_amdgcn_sched_group_barrier(0x100, READS * AHEAD, 0);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (i < N - AHEAD) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
-    __builtin_amdgcn_sched_group_barrier(0x400, 1, 0);
-  }
 }
 
 // Marks loaded fragments as arrived.  Without it the wait for them stands at their first
