@@ -6,8 +6,8 @@
 // and queries streamed.  The scores are formed twice (7 products where 5 would
 // do), which costs less than a fixed-order sum of dq over blocks of keys.
 //
-// Bound by the matrix cores and the vector units: 16 + 4 heads of 128, 8192 tokens, bf16: dq 435 us
-// (3 products, 0.95 PFLOP/s), dk/dv 724 us (4 products, 0.76 PFLOP/s).  dq has two waves on a
+// Bound by the matrix cores and the vector units: 16 + 4 heads of 128, 8192 tokens, bf16: dq 406 us
+// (3 products, 1.01 PFLOP/s), dk/dv 621 us (4 products, 0.89 PFLOP/s).  dq has two waves on a
 // SIMD (three with heads of 64).  dk/dv holds a key's and a value's row and both of their sums,
 // over 256 registers with heads of 128, so one wave has a SIMD for itself and its products are
 // put in an order that fills the gaps by hand.

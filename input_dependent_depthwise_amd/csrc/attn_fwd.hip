@@ -16,8 +16,8 @@ namespace {
 // so the accumulator is rarely rescaled.
 //
 // Bound by the matrix and the vector units, which two waves of a SIMD use in turn: 16 + 4 heads of
-// 128, 4 rows of 4096 tokens, bf16: 300 us, 0.92 PFLOP/s (46 % of the matrix cores' cycles, 45 % of the
-// vector units'); 12 heads of 64, 8 rows of 2048: 75 us, 0.69 PFLOP/s, the vector units 66 %
+// 128, 4 rows of 4096 tokens, bf16: 304 us, 0.90 PFLOP/s (47 % of the matrix cores' cycles, 45 % of the
+// vector units'); 12 heads of 64, 8 rows of 2048: 75 to 78 us with the card, 0.67 PFLOP/s, the vector units 66 %
 // busy with the exponentials and what surrounds them.  Tiles of 64 keys: 32 took 96 us where 64
 // take 82 (heads of 64, two waves), 128 took 123 (registers).
 constexpr float kSlack = 8.f;

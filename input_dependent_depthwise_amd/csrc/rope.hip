@@ -3,9 +3,10 @@
 // Bound by memory: each element is read and written once.  A block takes a few
 // tokens whole: its threads form the cosines and sines of each (token, pair) once, in LDS,
 // while their first vectors are on the way, and then walk over the heads, neighbouring lanes on
-// neighbouring vectors of the row (16384 tokens of 20 heads of 128, bf16: 34 us, 4.9 TB/s, 95 %
-// of a large copy's rate; a thread for a pair and token that walks over the heads: 41 us).  No table is read from memory, and the fp64 reduction of an
-// angle is paid once for all heads.
+// neighbouring vectors of the row (16384 tokens of 20 heads of 128, bf16, half of each turned: 34 to 38 us
+// with the card, 4.5 to 4.9 TB/s where a large copy has 5.2; fp32, whole heads: 63 us, 5.3 TB/s of which the
+// 256 MB cache serves a part; bf16 with a thread for a pair and token that walks over the heads: 41 us).  No table is
+// read from memory, and the fp64 reduction of an angle is paid once for all heads.
 #include <algorithm>
 
 #include "attn.h"
