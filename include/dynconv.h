@@ -354,7 +354,8 @@ typedef struct {
 /* Sizes of an attention call.  head_dim: whole 16-byte vectors (a multiple of
  * 8 for bf16, of 4 for fp32), at most 128.  n_heads % n_kv_heads == 0.
  * scale: the factor on q.k, 0 for 1 / sqrt(head_dim); else finite and at least
- * 2^-120 (the backward's fp32 sums start from lse / scale, which has to be finite).  cu_seqlens / n_seqs: packed documents as in dynconv_problem
+ * 2^-120 (the backward's fp32 sums start from lse / scale, which has to be
+ * finite).  cu_seqlens / n_seqs: packed documents as in dynconv_problem
  * (B must be 1); tokens from cu_seqlens[n_seqs] on, if there are any, belong
  * to no document.  Limits: T and B below 2^31, B * n_heads * ceil(T / 128) below
  * 2^24 (blocks of 256 threads, less than 2^32 threads in a launch), a row
