@@ -434,6 +434,31 @@ DYNCONV_API int dynconv_attn_bwd(const dynconv_attn *a, const dynconv_view *q, c
                                  const dynconv_view *dv, void *workspace, size_t workspace_bytes,
                                  hipStream_t stream);
 
+/* What a token sees of its sequence through a window: itself and the window - 1
+ * tokens before it, and the first `sinks` tokens of the sequence (or document).
+ * window >= 1; one that holds the whole row is no window.  sinks: 0 .. 128. */
+typedef struct {
+  int32_t window, sinks;
+} dynconv_window;
+
+/*
+ * dynconv_attn_fwd and dynconv_attn_bwd where i sees j only if i - j < window
+ * or j (from its document's start) < sinks: the same formulas over those j,
+ * the same arguments, and work in proportion to T (window + sinks).  The
+ * backward's workspace: at least dynconv_attn_window_bwd_workspace_bytes(a, w).
+ * The rounding of short rows (16 bits of p and ds) is that of rows whose window
+ * and sinks are no more than 64 together, too.
+ */
+DYNCONV_API int dynconv_attn_window_fwd(const dynconv_attn *a, const dynconv_window *w, const dynconv_view *q,
+                                        const dynconv_view *k, const dynconv_view *v, const dynconv_view *o,
+                                        float *lse, hipStream_t stream);
+DYNCONV_API size_t dynconv_attn_window_bwd_workspace_bytes(const dynconv_attn *a, const dynconv_window *w);
+DYNCONV_API int dynconv_attn_window_bwd(const dynconv_attn *a, const dynconv_window *w, const dynconv_view *q,
+                                        const dynconv_view *k, const dynconv_view *v, const dynconv_view *o,
+                                        const float *lse, const dynconv_view *d_o, const dynconv_view *dq,
+                                        const dynconv_view *dk, const dynconv_view *dv, void *workspace,
+                                        size_t workspace_bytes, hipStream_t stream);
+
 /*
  * One token for each of B sequences (a->T must be 1, cu_seqlens NULL), the
  * step that follows dynconv_decode.  lengths[b] (device int32) tokens of

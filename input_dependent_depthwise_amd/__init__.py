@@ -72,11 +72,16 @@ class Rotary(ctypes.Structure):
                 ("factor", ctypes.c_float), ("freqs", ctypes.c_void_p)]
 
 
+class Window(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+
+
 # names the C header declares; the CPU tests check each is exported
 EXPORTS = ("dynconv_fwd", "dynconv_fwd_proj", "dynconv_fwd_noalloc", "dynconv_bwd", "dynconv_decode", "dynconv_workspace_bytes",
            "dynconv_gen_cache_bytes", "dynconv_status_str", "dynconv_abi_version", "dynconv_trace_next",
            "dynconv_rope_freqs", "dynconv_rope", "dynconv_attn_fwd", "dynconv_attn_bwd_workspace_bytes",
-           "dynconv_attn_bwd", "dynconv_attn_decode_workspace_bytes", "dynconv_attn_decode")
+           "dynconv_attn_bwd", "dynconv_attn_decode_workspace_bytes", "dynconv_attn_decode",
+           "dynconv_attn_window_fwd", "dynconv_attn_window_bwd_workspace_bytes", "dynconv_attn_window_bwd")
 DYNCONV_E_SCRATCH = -10
 NOALLOC_SCRATCH_BYTES = 16 << 20  # the static scratch of dynconv_fwd_noalloc
 
@@ -126,6 +131,11 @@ def lib() -> ctypes.CDLL:
         L.dynconv_attn_decode_workspace_bytes.argtypes = [PA, I64]
         L.dynconv_attn_decode_workspace_bytes.restype = SZ
         L.dynconv_attn_decode.argtypes = [PA, PR, PV, PV, PV, PV, PV, I64, P, PV, P, SZ, P]
+        PW = P  # Window, likewise
+        L.dynconv_attn_window_fwd.argtypes = [PA, PW, PV, PV, PV, PV, P, P]
+        L.dynconv_attn_window_bwd_workspace_bytes.argtypes = [PA, PW]
+        L.dynconv_attn_window_bwd_workspace_bytes.restype = SZ
+        L.dynconv_attn_window_bwd.argtypes = [PA, PW, PV, PV, PV, PV, P, PV, PV, PV, PV, P, SZ, P]
         _lib = L
     return _lib
 
@@ -358,6 +368,16 @@ class DynConvFn(torch.autograd.Function):
 # raw stream is asked for, 12 us a rotary call -> 8.
 
 _VIEW, _ATTN, _ROTARY = struct.Struct("Pqqq").pack, struct.Struct("qqiiiifiPq").pack, struct.Struct("iiifP").pack
+_WINDOW = struct.Struct("ii").pack
+_MOST_TOKENS = 2 ** 31 - 1
+
+
+def _pack_window(window, sinks) -> bytes:
+    if not (isinstance(window, int) and isinstance(sinks, int)):
+        raise TypeError(f"window and sinks must be whole numbers, got {window!r} and {sinks!r}")
+    if window < 1 or not 0 <= sinks <= 128:
+        raise ValueError(f"window must be 1 or more and sinks 0 to 128, got {window} and {sinks}")
+    return _WINDOW(min(window, _MOST_TOKENS), sinks)
 
 
 def _pack_view(t: torch.Tensor, what: str, shape, dtype, dev: int) -> bytes:
@@ -506,6 +526,21 @@ def dynconv_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, o=None, lse=None, 
     1 / sqrt(head_dim).  cu_seqlens: packed documents (B must be 1)."""
     if stream is not None:
         return _on(stream, dynconv_attn_fwd, q, k, v, scale=scale, cu_seqlens=cu_seqlens, o=o, lse=lse, want_lse=want_lse)
+    return _forward("dynconv_attn_fwd", (), q, k, v, scale, cu_seqlens, o, lse, want_lse)
+
+
+def dynconv_attn_window_fwd(q, k, v, window, *, sinks=0, scale=None, cu_seqlens=None, o=None, lse=None, want_lse=False,
+                            stream=None):
+    """dynconv_attn_fwd where a token sees itself and the ``window`` - 1 tokens
+    before it, and the first ``sinks`` (0 to 128) tokens of its sequence or
+    document."""
+    if stream is not None:
+        return _on(stream, dynconv_attn_window_fwd, q, k, v, window, sinks=sinks, scale=scale, cu_seqlens=cu_seqlens, o=o,
+                   lse=lse, want_lse=want_lse)
+    return _forward("dynconv_attn_window_fwd", (_pack_window(window, sinks),), q, k, v, scale, cu_seqlens, o, lse, want_lse)
+
+
+def _forward(name, window, q, k, v, scale, cu_seqlens, o, lse, want_lse):
     B, T, H, hd = shape = _dims(q, "q", 4)
     G, dt, dev = _dims(k, "k", 4)[2], q.dtype, q.get_device()
     kv = (B, T, G, hd)
@@ -518,7 +553,7 @@ def dynconv_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, o=None, lse=None, 
         pl = lse.data_ptr()
     else:
         pl = None
-    _launch(dev, "dynconv_attn_fwd", lib().dynconv_attn_fwd, a, vq, _pack_view(k, "k", kv, dt, dev),
+    _launch(dev, name, getattr(lib(), name), a, *window, vq, _pack_view(k, "k", kv, dt, dev),
             _pack_view(v, "v", kv, dt, dev), vo, pl)
     return (o, lse) if want_lse else o
 
@@ -530,6 +565,21 @@ def dynconv_attn_bwd(q, k, v, o, lse, d_o, *, scale=None, cu_seqlens=None, out=N
     if stream is not None:
         return _on(stream, dynconv_attn_bwd, q, k, v, o, lse, d_o, scale=scale, cu_seqlens=cu_seqlens, out=out,
                    workspace=workspace)
+    return _backward("dynconv_attn_bwd", (), q, k, v, o, lse, d_o, scale, cu_seqlens, out, workspace)
+
+
+def dynconv_attn_window_bwd(q, k, v, o, lse, d_o, window, *, sinks=0, scale=None, cu_seqlens=None, out=None,
+                            workspace=None, stream=None):
+    """Backward of dynconv_attn_window_fwd, as dynconv_attn_bwd is of
+    dynconv_attn_fwd."""
+    if stream is not None:
+        return _on(stream, dynconv_attn_window_bwd, q, k, v, o, lse, d_o, window, sinks=sinks, scale=scale,
+                   cu_seqlens=cu_seqlens, out=out, workspace=workspace)
+    return _backward("dynconv_attn_window_bwd", (_pack_window(window, sinks),), q, k, v, o, lse, d_o, scale, cu_seqlens,
+                     out, workspace)
+
+
+def _backward(name, window, q, k, v, o, lse, d_o, scale, cu_seqlens, out, workspace):
     B, T, H, hd = shape = _dims(q, "q", 4)
     G, dt, dev = _dims(k, "k", 4)[2], q.dtype, q.get_device()
     kv = (B, T, G, hd)
@@ -541,8 +591,8 @@ def dynconv_attn_bwd(q, k, v, o, lse, d_o, *, scale=None, cu_seqlens=None, out=N
     dk, vdk = _out(out.get("dk"), k, "dk", kv, dev)
     dv, vdv = _out(out.get("dv"), v, "dv", kv, dev)
     L = lib()
-    ws = _workspace(L.dynconv_attn_bwd_workspace_bytes(a), q.device, workspace)
-    _launch(dev, "dynconv_attn_bwd", L.dynconv_attn_bwd, a, *ins, vdq, vdk, vdv, ws.data_ptr(), ws.nbytes)
+    ws = _workspace(getattr(L, name + "_workspace_bytes")(a, *window), q.device, workspace)
+    _launch(dev, name, getattr(L, name), a, *window, *ins, vdq, vdk, vdv, ws.data_ptr(), ws.nbytes)
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
@@ -577,37 +627,47 @@ def dynconv_attn_decode(q, k, v, k_cache, v_cache, lengths, *, scale=None, freqs
 
 class QKVAttnFn(torch.autograd.Function):
     """autograd wrapper of what follows the convolution on the Q/K/V path:
-    o = QKVAttnFn.apply(row, n_heads, n_kv_heads, freqs[, interleaved, factor, scale, cu_seqlens]).
+    o = QKVAttnFn.apply(row, n_heads, n_kv_heads, freqs[, interleaved, factor, scale, cu_seqlens, window, sinks]).
 
     row [B, T, (n_heads + 2 n_kv_heads) head_dim] (query, key and value heads
     side by side, as DynConvFn returns it) -> rotary positions on its query and
-    key heads (freqs None: none) -> causal attention -> o [B, T, n_heads, head_dim].
+    key heads (freqs None: none) -> causal attention (window None: over all
+    earlier tokens) -> o [B, T, n_heads, head_dim].
     The backward writes one gradient row, turned back in place.  First derivatives only.
     """
 
     @staticmethod
-    def forward(ctx, row, n_heads, n_kv_heads, freqs, interleaved=False, factor=1.0, scale=None, cu_seqlens=None):
+    def forward(ctx, row, n_heads, n_kv_heads, freqs, interleaved=False, factor=1.0, scale=None, cu_seqlens=None,
+                window=None, sinks=0):
         H, G = n_heads, n_kv_heads
         heads = row.view(row.shape[0], row.shape[1], H + 2 * G, row.shape[2] // (H + 2 * G))
         qk, v = heads[:, :, :H + G], heads[:, :, H + G:]
         if freqs is not None:
             qk = dynconv_rope(qk, freqs, cu_seqlens=cu_seqlens, interleaved=interleaved, factor=factor)
-        o, lse = dynconv_attn_fwd(qk[:, :, :H], qk[:, :, H:], v, scale=scale, cu_seqlens=cu_seqlens, want_lse=True)
+        if window is None:
+            o, lse = dynconv_attn_fwd(qk[:, :, :H], qk[:, :, H:], v, scale=scale, cu_seqlens=cu_seqlens, want_lse=True)
+        else:
+            o, lse = dynconv_attn_window_fwd(qk[:, :, :H], qk[:, :, H:], v, window, sinks=sinks, scale=scale,
+                                             cu_seqlens=cu_seqlens, want_lse=True)
         ctx.save_for_backward(qk, v, o, lse, freqs, cu_seqlens)
-        ctx.args = H, interleaved, factor, scale
+        ctx.args = H, interleaved, factor, scale, window, sinks
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_o):
         qk, v, o, lse, freqs, cu_seqlens = ctx.saved_tensors
-        H, interleaved, factor, scale = ctx.args
+        H, interleaved, factor, scale, window, sinks = ctx.args
         both = qk.shape[2]
         B, T, heads, hd = qk.shape[0], qk.shape[1], both + v.shape[2], qk.shape[3]
         row = torch.empty((B, T, heads, hd), dtype=qk.dtype, device=qk.device)
-        dynconv_attn_bwd(qk[:, :, :H], qk[:, :, H:], v, o, lse, d_o.contiguous(), scale=scale, cu_seqlens=cu_seqlens,
-                         out={"dq": row[:, :, :H], "dk": row[:, :, H:both], "dv": row[:, :, both:]})
+        ins = qk[:, :, :H], qk[:, :, H:], v, o, lse, d_o.contiguous()
+        out = {"dq": row[:, :, :H], "dk": row[:, :, H:both], "dv": row[:, :, both:]}
+        if window is None:
+            dynconv_attn_bwd(*ins, scale=scale, cu_seqlens=cu_seqlens, out=out)
+        else:
+            dynconv_attn_window_bwd(*ins, window, sinks=sinks, scale=scale, cu_seqlens=cu_seqlens, out=out)
         if freqs is not None:
             dynconv_rope(row[:, :, :both], freqs, cu_seqlens=cu_seqlens, interleaved=interleaved, factor=factor,
                          inverse=True, out=row[:, :, :both])
-        return (row.view(B, T, heads * hd),) + (None,) * 7
+        return (row.view(B, T, heads * hd),) + (None,) * 9

@@ -38,6 +38,7 @@ FILE_FLAGS = {
     # one wave per SIMD holds more than 256 registers here: without it every score block is copied
     # between the two halves of the register file
     "attn_bwd_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "attn_window_bwd_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

@@ -35,6 +35,8 @@ struct AttnArgs {
   float scale;
   const int32_t *cu;
   int n_seqs;
+  int window, sinks;  // the windowed kernels: a query sees the last `window` tokens and the first `sinks` of its document
+  float *far;         // their backward: dk / dv of sinks from the queries past their window, see far_rows
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -389,6 +391,48 @@ __device__ __forceinline__ void write_row(char *row, const f32x16 (&acc)[DH / 32
   for (int d = 0; d < DH / 32; ++d) write_part<T>(row, acc[d], d, f, hd, lane);
 }
 
+// Which keys the queries of the forward and dq kernels see of their document (WIN false: all earlier ones), and
+// with that the order of a block's key tiles: those of the sinks, if they lie before the window, then the window's.
+template <int BN, bool WIN>
+struct Window {
+  __device__ __forceinline__ void begin(const AttnArgs &, int, int, int, int &) {}
+  __device__ __forceinline__ bool sees(int) const { return true; }
+  __device__ __forceinline__ bool part(int, int, int) const { return false; }
+  __device__ __forceinline__ bool none(int, int, int) const { return false; }
+  __device__ __forceinline__ int after(int kt) const { return kt + BN; }
+  __device__ __forceinline__ int tile(int first, int i) const { return first + BN * i; }
+};
+template <int BN>
+struct Window<BN, true> {
+  int size, sinks;     // the window's tokens, and the first ones of a document
+  int hop_at, hop_to;  // the window's part of the tiles, see window_keys
+  int from, until;     // the lane's query sees keys >= from and keys < until
+  // q0: the block's first query; q, start: the lane's query and its document's start; first: the document's start of q0,
+  // the block's first key afterwards
+  __device__ __forceinline__ void begin(const AttnArgs &a, int q0, int q, int start, int &first) {
+    size = a.window;
+    sinks = a.sinks;
+    window_keys(size, sinks, BN, q0, first, hop_at, hop_to);
+    from = q - size + 1;
+    until = start + sinks;
+  }
+  __device__ __forceinline__ bool sees(int key) const { return key >= from || key < until; }
+  // Whether some of the 32 queries from qw on might not see some key of the tile; w_first: where lane 0's document starts
+  // (the others' sinks end no earlier).
+  __device__ __forceinline__ bool part(int kt, int qw, int w_first) const {
+    return kt <= qw + 31 - size && kt + BN > w_first + sinks;
+  }
+  // Whether none of them sees any (a query of a later document than lane 0's has all of its earlier tokens past qw).
+  __device__ __forceinline__ bool none(int kt, int qw, int w_first) const {
+    return kt + BN <= qw - size + 1 && kt >= w_first + sinks;
+  }
+  __device__ __forceinline__ int after(int kt) const { return kt + BN == hop_at ? hop_to : kt + BN; }
+  __device__ __forceinline__ int tile(int first, int i) const {
+    const int kt = first + BN * i;
+    return hop_at < 0 || kt < hop_at ? kt : hop_to + (kt - hop_at);
+  }
+};
+
 // Waves of the forward and dq kernels on a SIMD: as many as the registers of a wave allow (3 and not 2
 // for bf16 heads of 64: 12 heads, 8 rows of 2048 tokens, forward 81 -> 75 us; 1 for rows of 512 bytes,
 // whose owned rows alone take 128 registers).
@@ -420,6 +464,11 @@ template <typename T>
 inline bool with_rest(const AttnArgs &a) {
   return sizeof(T) == 2 && a.T <= 64 * (int64_t)(a.cu ? a.n_seqs : 1);
 }
+// The same for a window: a row of any length has few keys where the window and the sinks are few.
+template <typename T>
+inline bool with_rest_window(const AttnArgs &a) {
+  return with_rest<T>(a) || (sizeof(T) == 2 && (int64_t)a.window + a.sinks <= 64);
+}
 
 template <typename T, int DH>
 struct FewLds {
@@ -450,7 +499,18 @@ __device__ __forceinline__ void block_of(int n_heads_all, int &tile_rank, int &h
   }
 }
 
+// Rows of AttnArgs::far: sinks' sums of the queries past their window, [B][G][chunk][slot of its document][sink], one
+// slot a chunk without packing; none where no query lies past the window of the first 128 keys.
+__host__ __device__ __forceinline__ int far_slots(const AttnArgs &a) { return a.cu ? kFarSlots : 1; }
+inline bool has_far(const AttnArgs &a) { return a.sinks > 0 && a.T > (int64_t)a.window + 127; }
+inline int64_t far_rows(const AttnArgs &a) {
+  return has_far(a) ? (int64_t)a.B * a.G * ((a.T + kFarChunk - 1) / kFarChunk) * far_slots(a) * a.sinks : 0;
+}
+
 int attn_fwd(const AttnArgs &a, int dtype, hipStream_t st);
+int attn_window_fwd(const AttnArgs &a, int dtype, hipStream_t st);
+int attn_window_bwd(const AttnArgs &a, int dtype, hipStream_t st);
+int attn_window_bwd_fp32(const AttnArgs &a, hipStream_t st);
 int attn_bwd(const AttnArgs &a, int dtype, hipStream_t st);
 int attn_bwd_fp32(const AttnArgs &a, hipStream_t st);
 // blocks that share the (query head, query tile) pairs of a tile of keys in the dk/dv kernel

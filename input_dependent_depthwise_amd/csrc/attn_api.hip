@@ -147,22 +147,121 @@ AttnArgs attn_args(const dynconv_attn *a) {
 inline int attn_status() { return hipGetLastError() == hipSuccess ? DYNCONV_OK : DYNCONV_E_HIP; }
 inline int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// Backward workspace: delta, then the partial dk / dv.
+constexpr int kMaxSinks = 128;  // (the backward sums them apart: at most two blocks of 128 keys hold a document's)
+
+int check_window(const dynconv_window *w) {
+  if (!w) return DYNCONV_E_NULL;
+  if (w->window < 1 || w->sinks < 0) return DYNCONV_E_SHAPE;
+  return w->sinks > kMaxSinks ? DYNCONV_E_LIMIT : DYNCONV_OK;
+}
+
+// Backward workspace: delta, then the partial dk / dv, then those of the sinks.
 struct BwdPlan {
   int splits;
-  int64_t delta, part;
+  int64_t delta, part, far;
+  int64_t bytes() const { return delta + part + far; }
 };
-BwdPlan bwd_plan(const dynconv_attn *a) {
+BwdPlan bwd_plan(const dynconv_attn *a, const dynconv_window *w) {
   BwdPlan p;
-  p.splits = attn_bwd_splits(attn_args(a), a->dtype);
+  AttnArgs r = attn_args(a);
+  r.window = w ? w->window : 0;
+  r.sinks = w ? w->sinks : 0;
+  p.splits = attn_bwd_splits(r, a->dtype);
   p.delta = pad256(a->B * a->n_heads * a->T * 4);
-  p.part = p.splits > 1 ? (int64_t)2 * p.splits * a->B * a->n_kv_heads * a->T * a->head_dim * 4 : 0;
+  p.part = p.splits > 1 ? pad256((int64_t)2 * p.splits * a->B * a->n_kv_heads * a->T * a->head_dim * 4) : 0;
+  p.far = w ? (int64_t)2 * far_rows(r) * a->head_dim * 4 : 0;
   return p;
 }
 
 int64_t decode_bytes(const dynconv_attn *a, int64_t capacity) {
   const int n = decode_splits(a->B, a->n_heads, a->n_kv_heads, capacity);
   return n > 1 ? a->B * a->n_heads * n * (a->head_dim + 2) * 4 : 0;
+}
+
+// The window, or none where it holds a whole row (every token then sees all of its document as it is).
+const dynconv_window *narrower(const dynconv_attn *a, const dynconv_window *w) {
+  return a && w->window >= a->T ? nullptr : w;
+}
+
+// w: NULL for no window
+int forward(const dynconv_attn *a, const dynconv_window *w, const dynconv_view *q, const dynconv_view *k,
+            const dynconv_view *v, const dynconv_view *o, float *lse, hipStream_t stream) {
+  int rc = check_attn(a, true);
+  if (rc) return rc;
+  if (a->B == 0 || a->T == 0) return DYNCONV_OK;
+  const int64_t eb = a->dtype == DYNCONV_BF16 ? 2 : 4, H = a->n_heads, G = a->n_kv_heads, hd = a->head_dim;
+  Extent xq, xk, xv, xo;
+  if ((rc = extent(q, a->B, a->T, H, hd, eb, true, xq)) || (rc = extent(k, a->B, a->T, G, hd, eb, true, xk)) ||
+      (rc = extent(v, a->B, a->T, G, hd, eb, true, xv)) || (rc = extent(o, a->B, a->T, H, hd, eb, true, xo)))
+    return rc;
+  if (lse && ((uintptr_t)lse & 3u) != 0) return DYNCONV_E_ALIGN;
+  const Extent xl = flat(lse, lse ? a->B * H * a->T * 4 : 0);
+  const Extent xc = flat(a->cu_seqlens, a->cu_seqlens ? (a->n_seqs + 1) * 4 : 0);
+  if (!disjoint_rows(xo)) return DYNCONV_E_ALIAS;
+  const Extent *ins[] = {&xq, &xk, &xv, &xc};
+  for (const Extent *i : ins) {
+    if (!i->p) continue;
+    if (meet(xo, *i) || (lse && meet(xl, *i))) return DYNCONV_E_ALIAS;
+  }
+  if (lse && meet(xo, xl)) return DYNCONV_E_ALIAS;
+  AttnArgs r = attn_args(a);
+  r.q = strided(xq);
+  r.k = strided(xk);
+  r.v = strided(xv);
+  r.o = strided(xo);
+  r.lse = lse;
+  r.window = w ? w->window : 0;
+  r.sinks = w ? w->sinks : 0;
+  if ((rc = w ? attn_window_fwd(r, a->dtype, stream) : attn_fwd(r, a->dtype, stream))) return rc;
+  return attn_status();
+}
+
+int backward(const dynconv_attn *a, const dynconv_window *w, const dynconv_view *q, const dynconv_view *k,
+             const dynconv_view *v, const dynconv_view *o, const float *lse, const dynconv_view *d_o,
+             const dynconv_view *dq, const dynconv_view *dk, const dynconv_view *dv, void *workspace,
+             size_t workspace_bytes, hipStream_t stream) {
+  int rc = check_attn(a, true);
+  if (rc) return rc;
+  if (a->B == 0 || a->T == 0) return DYNCONV_OK;
+  const int64_t eb = a->dtype == DYNCONV_BF16 ? 2 : 4, H = a->n_heads, G = a->n_kv_heads, hd = a->head_dim;
+  if (!lse) return DYNCONV_E_NULL;
+  const dynconv_view *views[] = {q, k, v, o, d_o, dq, dk, dv};
+  const int64_t heads[] = {H, G, G, H, H, H, G, G};
+  Extent x[8];
+  for (int i = 0; i < 8; ++i)
+    if ((rc = extent(views[i], a->B, a->T, heads[i], hd, eb, true, x[i]))) return rc;
+  if (((uintptr_t)lse & 3u) != 0 || ((uintptr_t)workspace & 15u) != 0) return DYNCONV_E_ALIGN;
+  const BwdPlan p = bwd_plan(a, w);
+  if (!workspace || workspace_bytes < (size_t)p.bytes()) return DYNCONV_E_WORKSPACE;
+  const Extent xl = flat(lse, a->B * H * a->T * 4);
+  const Extent xc = flat(a->cu_seqlens, a->cu_seqlens ? (a->n_seqs + 1) * 4 : 0);
+  const Extent xw = flat(workspace, p.bytes());
+  const Extent *ins[] = {&x[0], &x[1], &x[2], &x[3], &x[4], &xl, &xc}, *outs[] = {&x[5], &x[6], &x[7], &xw};
+  for (int i = 0; i < 4; ++i) {
+    if (i < 3 && !disjoint_rows(*outs[i])) return DYNCONV_E_ALIAS;
+    for (const Extent *n : ins)
+      if (n->p && meet(*outs[i], *n)) return DYNCONV_E_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (meet(*outs[i], *outs[j])) return DYNCONV_E_ALIAS;
+  }
+  AttnArgs r = attn_args(a);
+  r.q = strided(x[0]);
+  r.k = strided(x[1]);
+  r.v = strided(x[2]);
+  r.o = strided(x[3]);
+  r.d_o = strided(x[4]);
+  r.dq = strided(x[5]);
+  r.dk = strided(x[6]);
+  r.dv = strided(x[7]);
+  r.lse = const_cast<float *>(lse);
+  r.delta = (float *)workspace;
+  r.part = (float *)((char *)workspace + p.delta);
+  r.far = (float *)((char *)workspace + p.delta + p.part);
+  r.n_split = p.splits;
+  r.window = w ? w->window : 0;
+  r.sinks = w ? w->sinks : 0;
+  if ((rc = w ? attn_window_bwd(r, a->dtype, stream) : attn_bwd(r, a->dtype, stream))) return rc;
+  return attn_status();
 }
 
 }  // namespace
@@ -246,83 +345,39 @@ int dynconv_rope(const dynconv_attn *a, const dynconv_rotary *r, const dynconv_v
 
 int dynconv_attn_fwd(const dynconv_attn *a, const dynconv_view *q, const dynconv_view *k, const dynconv_view *v,
                      const dynconv_view *o, float *lse, hipStream_t stream) {
-  int rc = check_attn(a, true);
-  if (rc) return rc;
-  if (a->B == 0 || a->T == 0) return DYNCONV_OK;
-  const int64_t eb = a->dtype == DYNCONV_BF16 ? 2 : 4, H = a->n_heads, G = a->n_kv_heads, hd = a->head_dim;
-  Extent xq, xk, xv, xo;
-  if ((rc = extent(q, a->B, a->T, H, hd, eb, true, xq)) || (rc = extent(k, a->B, a->T, G, hd, eb, true, xk)) ||
-      (rc = extent(v, a->B, a->T, G, hd, eb, true, xv)) || (rc = extent(o, a->B, a->T, H, hd, eb, true, xo)))
-    return rc;
-  if (lse && ((uintptr_t)lse & 3u) != 0) return DYNCONV_E_ALIGN;
-  const Extent xl = flat(lse, lse ? a->B * H * a->T * 4 : 0);
-  const Extent xc = flat(a->cu_seqlens, a->cu_seqlens ? (a->n_seqs + 1) * 4 : 0);
-  if (!disjoint_rows(xo)) return DYNCONV_E_ALIAS;
-  const Extent *ins[] = {&xq, &xk, &xv, &xc};
-  for (const Extent *i : ins) {
-    if (!i->p) continue;
-    if (meet(xo, *i) || (lse && meet(xl, *i))) return DYNCONV_E_ALIAS;
-  }
-  if (lse && meet(xo, xl)) return DYNCONV_E_ALIAS;
-  AttnArgs r = attn_args(a);
-  r.q = strided(xq);
-  r.k = strided(xk);
-  r.v = strided(xv);
-  r.o = strided(xo);
-  r.lse = lse;
-  if ((rc = attn_fwd(r, a->dtype, stream))) return rc;
-  return attn_status();
+  return forward(a, nullptr, q, k, v, o, lse, stream);
+}
+
+int dynconv_attn_window_fwd(const dynconv_attn *a, const dynconv_window *w, const dynconv_view *q,
+                            const dynconv_view *k, const dynconv_view *v, const dynconv_view *o, float *lse,
+                            hipStream_t stream) {
+  const int rc = check_window(w);
+  return rc ? rc : forward(a, narrower(a, w), q, k, v, o, lse, stream);
 }
 
 size_t dynconv_attn_bwd_workspace_bytes(const dynconv_attn *a) {
   if (check_attn(a, true) || a->B == 0 || a->T == 0) return 0;
-  const BwdPlan p = bwd_plan(a);
-  return (size_t)(p.delta + p.part);
+  return (size_t)bwd_plan(a, nullptr).bytes();
+}
+
+size_t dynconv_attn_window_bwd_workspace_bytes(const dynconv_attn *a, const dynconv_window *w) {
+  if (check_window(w) || check_attn(a, true) || a->B == 0 || a->T == 0) return 0;
+  return (size_t)bwd_plan(a, narrower(a, w)).bytes();
 }
 
 int dynconv_attn_bwd(const dynconv_attn *a, const dynconv_view *q, const dynconv_view *k, const dynconv_view *v,
                      const dynconv_view *o, const float *lse, const dynconv_view *d_o, const dynconv_view *dq,
                      const dynconv_view *dk, const dynconv_view *dv, void *workspace, size_t workspace_bytes,
                      hipStream_t stream) {
-  int rc = check_attn(a, true);
-  if (rc) return rc;
-  if (a->B == 0 || a->T == 0) return DYNCONV_OK;
-  const int64_t eb = a->dtype == DYNCONV_BF16 ? 2 : 4, H = a->n_heads, G = a->n_kv_heads, hd = a->head_dim;
-  if (!lse) return DYNCONV_E_NULL;
-  const dynconv_view *views[] = {q, k, v, o, d_o, dq, dk, dv};
-  const int64_t heads[] = {H, G, G, H, H, H, G, G};
-  Extent x[8];
-  for (int i = 0; i < 8; ++i)
-    if ((rc = extent(views[i], a->B, a->T, heads[i], hd, eb, true, x[i]))) return rc;
-  if (((uintptr_t)lse & 3u) != 0 || ((uintptr_t)workspace & 15u) != 0) return DYNCONV_E_ALIGN;
-  const BwdPlan p = bwd_plan(a);
-  if (!workspace || workspace_bytes < (size_t)(p.delta + p.part)) return DYNCONV_E_WORKSPACE;
-  const Extent xl = flat(lse, a->B * H * a->T * 4);
-  const Extent xc = flat(a->cu_seqlens, a->cu_seqlens ? (a->n_seqs + 1) * 4 : 0);
-  const Extent xw = flat(workspace, p.delta + p.part);
-  const Extent *ins[] = {&x[0], &x[1], &x[2], &x[3], &x[4], &xl, &xc}, *outs[] = {&x[5], &x[6], &x[7], &xw};
-  for (int i = 0; i < 4; ++i) {
-    if (i < 3 && !disjoint_rows(*outs[i])) return DYNCONV_E_ALIAS;
-    for (const Extent *n : ins)
-      if (n->p && meet(*outs[i], *n)) return DYNCONV_E_ALIAS;
-    for (int j = 0; j < i; ++j)
-      if (meet(*outs[i], *outs[j])) return DYNCONV_E_ALIAS;
-  }
-  AttnArgs r = attn_args(a);
-  r.q = strided(x[0]);
-  r.k = strided(x[1]);
-  r.v = strided(x[2]);
-  r.o = strided(x[3]);
-  r.d_o = strided(x[4]);
-  r.dq = strided(x[5]);
-  r.dk = strided(x[6]);
-  r.dv = strided(x[7]);
-  r.lse = const_cast<float *>(lse);
-  r.delta = (float *)workspace;
-  r.part = (float *)((char *)workspace + p.delta);
-  r.n_split = p.splits;
-  if ((rc = attn_bwd(r, a->dtype, stream))) return rc;
-  return attn_status();
+  return backward(a, nullptr, q, k, v, o, lse, d_o, dq, dk, dv, workspace, workspace_bytes, stream);
+}
+
+int dynconv_attn_window_bwd(const dynconv_attn *a, const dynconv_window *w, const dynconv_view *q,
+                            const dynconv_view *k, const dynconv_view *v, const dynconv_view *o, const float *lse,
+                            const dynconv_view *d_o, const dynconv_view *dq, const dynconv_view *dk,
+                            const dynconv_view *dv, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int rc = check_window(w);
+  return rc ? rc : backward(a, narrower(a, w), q, k, v, o, lse, d_o, dq, dk, dv, workspace, workspace_bytes, stream);
 }
 
 size_t dynconv_attn_decode_workspace_bytes(const dynconv_attn *a, int64_t capacity) {

@@ -1,4 +1,6 @@
 // attn_bwd_bf16.hip -- the attention backward for bf16 tensors, and its dispatch.
+#include <algorithm>
+
 #include "attn_bwd.h"
 
 namespace dynconv {
@@ -10,7 +12,10 @@ namespace dynconv {
 // 1024 tokens (96 blocks, 16 tiles) 46, 44, 42, 47; 4 rows of 512 tokens (192, 8 tiles) 38, 48,
 // 54, 69.
 int attn_bwd_splits(const AttnArgs &a, int dtype) {
-  const double blocks = (double)((a.T + 127) / 128) * a.G * a.B, tiles = (double)((a.T + 63) / 64) * (a.H / a.G);
+  const double blocks = (double)((a.T + 127) / 128) * a.G * a.B;
+  // (through a window a block of keys has the queries of the window and its own)
+  const int64_t queries = a.window ? std::min<int64_t>(a.T, (int64_t)a.window + 127) : a.T;
+  const double tiles = (double)((queries + 63) / 64) * (a.H / a.G);
   const double tile_us = (dtype == DYNCONV_BF16 ? 1.0 : 8.0) * (a.hd <= 64 ? 1.4 : a.hd <= 96 ? 2.1 : 2.8);
   const double split_us = 16.0 * a.B * a.T * a.G * a.hd / 4.5e6, join_us = 4.0;
   int best = 1;
@@ -25,11 +30,8 @@ int attn_bwd_splits(const AttnArgs &a, int dtype) {
   return best;
 }
 
-// (Heads of 80 on 96 columns against 128, 16 + 4 heads, 4 rows of 4096 tokens: 868 against 1010 us.)
 int attn_bwd(const AttnArgs &a, int dtype, hipStream_t st) {
-  if (dtype != DYNCONV_BF16) return attn_bwd_fp32(a, st);
-  if (a.hd <= 64) return launch<bf16, 64, 64>(a, st);
-  return a.hd <= 96 ? launch<bf16, 96, 64>(a, st) : launch<bf16, 128, 64>(a, st);
+  return dtype == DYNCONV_BF16 ? dispatch_bf16<false>(a, st) : attn_bwd_fp32(a, st);
 }
 
 }  // namespace dynconv

@@ -57,6 +57,37 @@ __host__ __device__ __forceinline__ int queries_end(const int32_t *cu, int n_seq
   return end;
 }
 
+// The same through a window of `window` tokens with `sinks` first tokens of the document that stay visible, as
+// tiles of `tile` keys: first, first + tile, ... up to hop_at, from where they go on at hop_to, up to
+// last.  hop_at is below hop_to; without a gap between the two parts it is -1, and first is where
+// the one part starts.  Of the documents among the queries only the first one's sinks can lie before the
+// window of q0 (the others start behind q0).
+__host__ __device__ __forceinline__ void window_keys(int window, int sinks, int tile, int q0, int &first, int &hop_at,
+                                                     int &hop_to) {
+  hop_at = -1;
+  hop_to = greater(first, q0 - window + 1);
+  const int far = lesser(sinks, hop_to - first);  // sinks before the window
+  const int tiles = (far + tile - 1) / tile;
+  if (far == 0) first = hop_to;
+  else if (hop_to - first > tiles * tile) hop_at = first + tiles * tile;
+}
+
+// The queries that see keys k0 .. k0 + rows - 1 through the window: below this one (`end`, the end of the last
+// key's document, or less).  Sinks among the keys are seen by later queries as well.
+__host__ __device__ __forceinline__ int window_end(int window, int k0, int rows, int end) {
+  const int64_t w = (int64_t)k0 + rows - 1 + window;
+  return w < end ? (int)w : end;
+}
+
+// Queries past window_end of their block of 128 keys are taken in chunks of kFarChunk, a slot for the sums of each document that
+// has any in the chunk.  Such a document holds the last token of a block of 128 keys: the chunk's
+// first token belongs to the one of slot 0, and token 128 m - 1 of the chunk to the one of slot m if it starts inside.
+constexpr int kFarChunk = 512, kFarSlots = kFarChunk / 128;
+__host__ __device__ __forceinline__ int far_slot(int chunk, int start) {
+  const int c0 = chunk * kFarChunk;
+  return start <= c0 ? 0 : (start - c0) / 128 + 1;
+}
+
 // Bytes that a read of rows row0 .. limit - 1 (row_bytes apart, `len` bytes each) may reach from row0 on, at
 // most `most`; nothing when there is no such row.
 __host__ __device__ __forceinline__ uint32_t rows_extent(int row0, int limit, int64_t row_bytes, int len, uint32_t most) {
