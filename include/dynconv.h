@@ -483,6 +483,64 @@ DYNCONV_API int dynconv_attn_decode(const dynconv_attn *a, const dynconv_rotary 
                                     const dynconv_view *o, void *workspace, size_t workspace_bytes,
                                     hipStream_t stream);
 
+/*
+ * ---- A cache kept in pages ---------------------------------------------
+ *
+ * The keys and values of many sequences in one pool of pages, of which each
+ * sequence has a list: position j of sequence b is row j % page_size of page
+ * table[b][j / page_size].  What is past a sequence's tokens in its last page, and
+ * pages that no list names, are not read.
+ */
+typedef struct {
+  dynconv_view k, v;    /* pools [n_pages, page_size, n_kv_heads, head_dim]; batch is the stride of a page */
+  const int32_t *table; /* device int32 [sequences, pages_per_seq], 4-byte aligned           */
+  int64_t table_row;    /* elements from one sequence's list to the next one's                */
+  int64_t n_pages, pages_per_seq;
+  int32_t page_size;    /* any; pages_per_seq * page_size below 2^31 - 4096                   */
+  int32_t reserved;
+} dynconv_pages;
+
+/* The table is device data that the host cannot check.  An entry outside
+ * 0 .. n_pages-1 is no page: its tokens are not seen and what would be stored there is
+ * not.  So a list may be longer than what a sequence has, and pages that a window
+ * has left behind may be given back (their entries -1 or any other).  Sequences may
+ * share pages that they only read; a row that a call stores is to be in one list,
+ * once, or what the others read of it is unspecified. */
+
+/*
+ * The keys, turned by the rotary plan r (NULL: not turned; r->inverse must be
+ * 0), and values of prompts into their pages.  k, v [B, T, n_kv_heads,
+ * head_dim] (n_heads and scale of a are not used, but have to be valid):
+ *   token t < counts[b] (device int32 [B], NULL: T) of row b is position
+ *   starts[b] + t (device int32 [B], NULL: 0) of sequence b; with cu_seqlens
+ *   token t of the row, of document i, is position starts[i] + t - cu_seqlens[i]
+ *   of sequence i (counts must be NULL).
+ * The table has B (n_seqs) lists.  A sequence with starts < 0 is idle; tokens
+ * at positions past the list, or of no document, are not stored.  Keys are rounded
+ * to the I/O dtype once.  No workspace.
+ */
+DYNCONV_API int dynconv_attn_paged_store(const dynconv_attn *a, const dynconv_rotary *r, const dynconv_view *k,
+                                         const dynconv_view *v, const dynconv_pages *pages, const int32_t *starts,
+                                         const int32_t *counts, hipStream_t stream);
+
+/*
+ * dynconv_attn_decode over pages: one token for each of B sequences (a->T must
+ * be 1, cu_seqlens NULL) at position lengths[b].  q and k are turned, k and v
+ * stored in their page, and o = attention of q over the new token and those
+ * positions below lengths[b] that w lets it see (NULL: all) and that have a page.  The new
+ * token is seen whether or not it has one.  A slot with lengths[b] < 0 or
+ * >= pages_per_seq * page_size is idle: its o is zero, and nothing is stored.
+ * workspace: 16-byte aligned, at least
+ * dynconv_attn_paged_decode_workspace_bytes(a, w, pages); it may be 0 bytes.
+ * The size depends on the sizes in a, w and pages alone.
+ */
+DYNCONV_API size_t dynconv_attn_paged_decode_workspace_bytes(const dynconv_attn *a, const dynconv_window *w,
+                                                             const dynconv_pages *pages);
+DYNCONV_API int dynconv_attn_paged_decode(const dynconv_attn *a, const dynconv_window *w, const dynconv_rotary *r,
+                                          const dynconv_view *q, const dynconv_view *k, const dynconv_view *v,
+                                          const dynconv_pages *pages, const int32_t *lengths, const dynconv_view *o,
+                                          void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

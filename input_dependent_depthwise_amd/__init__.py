@@ -76,12 +76,19 @@ class Window(ctypes.Structure):
     _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
 
 
+class Pages(ctypes.Structure):
+    _fields_ = [("k", View), ("v", View), ("table", ctypes.c_void_p), ("table_row", ctypes.c_int64),
+                ("n_pages", ctypes.c_int64), ("pages_per_seq", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 # names the C header declares; the CPU tests check each is exported
 EXPORTS = ("dynconv_fwd", "dynconv_fwd_proj", "dynconv_fwd_noalloc", "dynconv_bwd", "dynconv_decode", "dynconv_workspace_bytes",
            "dynconv_gen_cache_bytes", "dynconv_status_str", "dynconv_abi_version", "dynconv_trace_next",
            "dynconv_rope_freqs", "dynconv_rope", "dynconv_attn_fwd", "dynconv_attn_bwd_workspace_bytes",
            "dynconv_attn_bwd", "dynconv_attn_decode_workspace_bytes", "dynconv_attn_decode",
-           "dynconv_attn_window_fwd", "dynconv_attn_window_bwd_workspace_bytes", "dynconv_attn_window_bwd")
+           "dynconv_attn_window_fwd", "dynconv_attn_window_bwd_workspace_bytes", "dynconv_attn_window_bwd",
+           "dynconv_attn_paged_store", "dynconv_attn_paged_decode_workspace_bytes", "dynconv_attn_paged_decode")
 DYNCONV_E_SCRATCH = -10
 NOALLOC_SCRATCH_BYTES = 16 << 20  # the static scratch of dynconv_fwd_noalloc
 
@@ -131,11 +138,15 @@ def lib() -> ctypes.CDLL:
         L.dynconv_attn_decode_workspace_bytes.argtypes = [PA, I64]
         L.dynconv_attn_decode_workspace_bytes.restype = SZ
         L.dynconv_attn_decode.argtypes = [PA, PR, PV, PV, PV, PV, PV, I64, P, PV, P, SZ, P]
-        PW = P  # Window, likewise
+        PW = PP = P  # Window and Pages, likewise
         L.dynconv_attn_window_fwd.argtypes = [PA, PW, PV, PV, PV, PV, P, P]
         L.dynconv_attn_window_bwd_workspace_bytes.argtypes = [PA, PW]
         L.dynconv_attn_window_bwd_workspace_bytes.restype = SZ
         L.dynconv_attn_window_bwd.argtypes = [PA, PW, PV, PV, PV, PV, P, PV, PV, PV, PV, P, SZ, P]
+        L.dynconv_attn_paged_store.argtypes = [PA, PR, PV, PV, PP, P, P, P]
+        L.dynconv_attn_paged_decode_workspace_bytes.argtypes = [PA, PW, PP]
+        L.dynconv_attn_paged_decode_workspace_bytes.restype = SZ
+        L.dynconv_attn_paged_decode.argtypes = [PA, PW, PR, PV, PV, PV, PP, P, PV, P, SZ, P]
         _lib = L
     return _lib
 
@@ -368,7 +379,7 @@ class DynConvFn(torch.autograd.Function):
 # raw stream is asked for, 12 us a rotary call -> 8.
 
 _VIEW, _ATTN, _ROTARY = struct.Struct("Pqqq").pack, struct.Struct("qqiiiifiPq").pack, struct.Struct("iiifP").pack
-_WINDOW = struct.Struct("ii").pack
+_WINDOW, _PAGES = struct.Struct("ii").pack, struct.Struct("PqqqPqqqPqqqii").pack
 _MOST_TOKENS = 2 ** 31 - 1
 
 
@@ -440,6 +451,22 @@ def _pack_rotary(freqs: torch.Tensor, interleaved, inverse, factor, dev) -> byte
     if freqs.get_device() != dev:
         _other_device(freqs, "freqs", dev)
     return _ROTARY(2 * freqs.shape[0], 1 if interleaved else 0, 1 if inverse else 0, factor, freqs.data_ptr())
+
+
+def _pack_pages(k_pages, v_pages, table, lists, G, hd, dtype, dev) -> bytes:
+    n, size = _dims(k_pages, "k_pages", 4)[:2]
+    pool = (n, size, G, hd)
+    for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _pack_view(t, what, pool, dtype, dev)
+    entry = table.stride()
+    if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2 or table.shape[0] != lists or (
+            entry[1] != 1 and table.shape[1] > 1):
+        raise TypeError(f"page_table must be an int32 tensor [{lists}, pages] on the GPU with a contiguous last axis")
+    if table.get_device() != dev:
+        _other_device(table, "page_table", dev)
+    sk, sv = k_pages.stride(), v_pages.stride()
+    return _PAGES(k_pages.data_ptr(), sk[0], sk[1], sk[2], v_pages.data_ptr(), sv[0], sv[1], sv[2], table.data_ptr(),
+                  entry[0], n, table.shape[1], size, 0)
 
 
 def _launch(dev: int, where: str, call, *args) -> None:
@@ -622,6 +649,64 @@ def dynconv_attn_decode(q, k, v, k_cache, v_cache, lengths, *, scale=None, freqs
             _pack_view(k, "k", kv, dt, dev), _pack_view(v, "v", kv, dt, dev),
             _pack_view(k_cache, "k_cache", rows, dt, dev), _pack_view(v_cache, "v_cache", rows, dt, dev), cap,
             _int32(lengths, "lengths", dev, (B,)), vo, _ptr(ws), 0 if ws is None else ws.nbytes)
+    return o
+
+
+def dynconv_attn_paged_store(k, v, k_pages, v_pages, page_table, *, starts=None, counts=None, cu_seqlens=None, freqs=None,
+                             interleaved=False, factor=1.0, stream=None):
+    """The keys, turned by the rotary plan (freqs None: not), and values of prompts
+    into a cache kept in pages: k and v [B, T, n_kv_heads, head_dim], pools
+    [n_pages, page_size, n_kv_heads, head_dim], page_table int32 [B, pages]
+    (position j of a sequence is row j % page_size of page page_table[b, j //
+    page_size]; an entry outside the pool is no page, nothing is stored there).
+    Token t < counts[b] (None: all) of row b becomes position starts[b] + t
+    (None: t); both int32 [B].  With cu_seqlens the documents of the single row
+    are the sequences.  Returns (k_pages, v_pages)."""
+    if stream is not None:
+        return _on(stream, dynconv_attn_paged_store, k, v, k_pages, v_pages, page_table, starts=starts, counts=counts,
+                   cu_seqlens=cu_seqlens, freqs=freqs, interleaved=interleaved, factor=factor)
+    B, T, G, hd = shape = _dims(k, "k", 4)
+    dt, dev = k.dtype, k.get_device()
+    vk, vv = _pack_view(k, "k", shape, dt, dev), _pack_view(v, "v", shape, dt, dev)
+    a = _pack_attn(B, T, G, G, hd, dt, dev, None, cu_seqlens)
+    lists = B if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    if counts is not None and cu_seqlens is not None:
+        raise ValueError("counts: the documents' lengths are given by cu_seqlens")
+    pages = _pack_pages(k_pages, v_pages, page_table, lists, G, hd, dt, dev)
+    _launch(dev, "dynconv_attn_paged_store", lib().dynconv_attn_paged_store, a,
+            None if freqs is None else _pack_rotary(freqs, interleaved, False, factor, dev), vk, vv, pages,
+            _int32(starts, "starts", dev, (lists,)), _int32(counts, "counts", dev, (lists,)))
+    return k_pages, v_pages
+
+
+def dynconv_attn_paged_decode(q, k, v, k_pages, v_pages, page_table, lengths, *, window=None, sinks=0, scale=None, freqs=None,
+                              interleaved=False, factor=1.0, o=None, workspace=None, stream=None):
+    """dynconv_attn_decode over a cache kept in pages (as dynconv_attn_paged_store
+    describes it): q [B, n_heads, head_dim], k and v [B, n_kv_heads, head_dim] of
+    the new tokens, at the positions lengths int32 [B].  window, sinks: the new
+    token sees itself, the ``window`` - 1 tokens before it and the first ``sinks``
+    (0 to 128) of its sequence (None: all); pages that hold none of these are not
+    read, and their entries in the table may be given up (-1)."""
+    if stream is not None:
+        return _on(stream, dynconv_attn_paged_decode, q, k, v, k_pages, v_pages, page_table, lengths, window=window,
+                   sinks=sinks, scale=scale, freqs=freqs, interleaved=interleaved, factor=factor, o=o,
+                   workspace=workspace)
+    B, H, hd = shape = _dims(q, "q", 3)
+    G, dt, dev = _dims(k, "k", 3)[1], q.dtype, q.get_device()
+    kv = (B, G, hd)
+    if window is None and sinks != 0:
+        raise ValueError("sinks need a window")
+    vq = _pack_view(q, "q", shape, dt, dev)
+    a, w = _pack_attn(B, 1, H, G, hd, dt, dev, scale, None), None if window is None else _pack_window(window, sinks)
+    pages = _pack_pages(k_pages, v_pages, page_table, B, G, hd, dt, dev)
+    o, vo = _out(o, q, "o", shape, dev)
+    L = lib()
+    nbytes = L.dynconv_attn_paged_decode_workspace_bytes(a, w, pages)
+    ws = _workspace(nbytes, q.device, workspace) if nbytes or workspace is not None else None
+    _launch(dev, "dynconv_attn_paged_decode", L.dynconv_attn_paged_decode, a, w,
+            None if freqs is None else _pack_rotary(freqs, interleaved, False, factor, dev), vq,
+            _pack_view(k, "k", kv, dt, dev), _pack_view(v, "v", kv, dt, dev), pages, _int32(lengths, "lengths", dev, (B,)),
+            vo, _ptr(ws), 0 if ws is None else ws.nbytes)
     return o
 
 

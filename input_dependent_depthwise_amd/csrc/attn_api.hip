@@ -6,6 +6,7 @@
 #include <algorithm>
 
 #include "attn_decode.h"
+#include "attn_paged.h"
 #include "kernels.h"
 #include "rope.h"
 
@@ -176,6 +177,68 @@ BwdPlan bwd_plan(const dynconv_attn *a, const dynconv_window *w) {
 int64_t decode_bytes(const dynconv_attn *a, int64_t capacity) {
   const int n = decode_splits(a->B, a->n_heads, a->n_kv_heads, capacity);
   return n > 1 ? a->B * a->n_heads * n * (a->head_dim + 2) * 4 : 0;
+}
+
+struct PoolExtents {
+  Extent k, v, table;
+};
+
+// lists: how many the table has.
+int check_pages(const dynconv_attn *a, const dynconv_pages *p, int64_t lists, PoolExtents &x) {
+  if (!p) return DYNCONV_E_NULL;
+  if (p->n_pages <= 0 || p->pages_per_seq <= 0 || p->page_size <= 0) return DYNCONV_E_SHAPE;
+  const int64_t lim = ((int64_t)1 << 31) - 4096;
+  if (p->n_pages > lim || p->pages_per_seq >= lim / p->page_size) return DYNCONV_E_LIMIT;
+  const int64_t eb = a->dtype == DYNCONV_BF16 ? 2 : 4, G = a->n_kv_heads, hd = a->head_dim;
+  int rc;
+  if ((rc = extent(&p->k, p->n_pages, p->page_size, G, hd, eb, true, x.k)) ||
+      (rc = extent(&p->v, p->n_pages, p->page_size, G, hd, eb, true, x.v)))
+    return rc;
+  if (!p->table) return DYNCONV_E_NULL;
+  if (((uintptr_t)p->table & 3u) != 0) return DYNCONV_E_ALIGN;
+  if (lists > 1 && p->table_row < 0) return DYNCONV_E_SHAPE;
+  if (lists > 1 && p->table_row > ((int64_t)1 << 58) / lists) return DYNCONV_E_LIMIT;
+  x.table = flat(p->table, ((lists - 1) * (lists > 1 ? p->table_row : 0) + p->pages_per_seq) * 4);
+  if (!disjoint_rows(x.k) || !disjoint_rows(x.v) || meet(x.k, x.v) || meet(x.k, x.table) || meet(x.v, x.table))
+    return DYNCONV_E_ALIAS;
+  return DYNCONV_OK;
+}
+
+Pages pages_of(const dynconv_pages *p, const PoolExtents &x) {
+  Pages r = {};
+  r.k = strided(x.k);
+  r.v = strided(x.v);
+  r.table = p->table;
+  r.table_row = p->table_row;
+  r.n_pages = (int)p->n_pages;
+  r.size = p->page_size;
+  r.per_seq = (int)p->pages_per_seq;
+  r.capacity = (int)(p->pages_per_seq * p->page_size);
+  return r;
+}
+
+// The sizes of a paged step, which is all that its workspace depends on.
+PagedArgs paged_args(const dynconv_attn *a, const dynconv_window *w, const Pages &pages) {
+  PagedArgs r = {};
+  r.pages = pages;
+  r.B = (int)a->B;
+  r.H = a->n_heads;
+  r.G = a->n_kv_heads;
+  r.hd = a->head_dim;
+  r.window = w && w->window < pages.capacity ? w->window : 0;
+  r.sinks = r.window ? w->sinks : 0;
+  r.blocks = paged_blocks(r);
+  return r;
+}
+
+int check_paged_decode(const dynconv_attn *a, const dynconv_window *w, const dynconv_pages *p, PoolExtents &x) {
+  int rc = check_attn(a, true);
+  if (rc || (w && (rc = check_window(w)))) return rc;
+  if (a->T != 1 || a->cu_seqlens) return DYNCONV_E_SHAPE;
+  if (a->B > 65535) return DYNCONV_E_LIMIT;
+  // blocks of 512 threads, below 2^32 threads in all
+  if (a->B * a->n_kv_heads * ((a->n_heads / a->n_kv_heads + 15) / 16) > ((int64_t)1 << 23) - 1) return DYNCONV_E_LIMIT;
+  return a->B == 0 ? DYNCONV_OK : check_pages(a, p, a->B, x);
 }
 
 // The window, or none where it holds a whole row (every token then sees all of its document as it is).
@@ -440,6 +503,103 @@ int dynconv_attn_decode(const dynconv_attn *a, const dynconv_rotary *rot, const 
   r.lengths = lengths;
   r.part = (float *)workspace;
   if ((rc = attn_decode(r, a->dtype, stream))) return rc;
+  return attn_status();
+}
+
+int dynconv_attn_paged_store(const dynconv_attn *a, const dynconv_rotary *rot, const dynconv_view *k,
+                             const dynconv_view *v, const dynconv_pages *pages, const int32_t *starts,
+                             const int32_t *counts, hipStream_t stream) {
+  int rc = check_attn(a, true);
+  if (rc || (rot && (rc = check_rotary(rot, a->head_dim)))) return rc;
+  if ((rot && rot->inverse) || (a->cu_seqlens && counts)) return DYNCONV_E_SHAPE;
+  if (a->B == 0 || a->T == 0) return DYNCONV_OK;
+  const int64_t lists = a->cu_seqlens ? a->n_seqs : a->B;
+  PoolExtents x;
+  if ((rc = check_pages(a, pages, lists, x))) return rc;
+  const int64_t eb = a->dtype == DYNCONV_BF16 ? 2 : 4, G = a->n_kv_heads, hd = a->head_dim;
+  Extent xk, xv;
+  if ((rc = extent(k, a->B, a->T, G, hd, eb, true, xk)) || (rc = extent(v, a->B, a->T, G, hd, eb, true, xv))) return rc;
+  if ((((uintptr_t)starts | (uintptr_t)counts) & 3u) != 0) return DYNCONV_E_ALIGN;
+  if (a->B > (((int64_t)1 << 31) - 4096) / a->T) return DYNCONV_E_LIMIT;
+  const Extent ins[] = {xk, xv, flat(starts, starts ? lists * 4 : 0), flat(counts, counts ? lists * 4 : 0),
+                        flat(a->cu_seqlens, a->cu_seqlens ? (a->n_seqs + 1) * 4 : 0),
+                        flat(rot ? rot->freqs : nullptr, rot ? rot->rot_dim / 2 * 8 : 0)};
+  for (const Extent &i : ins)
+    if (i.p && (meet(x.k, i) || meet(x.v, i))) return DYNCONV_E_ALIAS;
+  // the widest vector that the halves of the pairs are made of
+  const int64_t half = rot ? rot->rot_dim / 2 * eb : 0;
+  const int vec = half % 16 == 0 ? 16 : half % 8 == 0 ? 8 : 0;
+  PagedStoreArgs r = {};
+  r.k = strided(xk);
+  r.v = strided(xv);
+  r.pages = pages_of(pages, x);
+  r.B = (int)a->B;
+  r.T = (int)a->T;
+  r.G = a->n_kv_heads;
+  r.hd = a->head_dim;
+  r.rot = rot ? rot->rot_dim : 0;
+  r.interleaved = rot && rot->interleaved != 0;
+  r.factor = rot ? rot->factor : 1.f;
+  r.freqs = rot ? rot->freqs : nullptr;
+  r.starts = starts;
+  r.counts = counts;
+  r.cu = a->cu_seqlens;
+  r.n_seqs = a->cu_seqlens ? (int)a->n_seqs : 0;
+  if ((rc = attn_paged_store(r, a->dtype, vec, stream))) return rc;
+  return attn_status();
+}
+
+size_t dynconv_attn_paged_decode_workspace_bytes(const dynconv_attn *a, const dynconv_window *w,
+                                                 const dynconv_pages *pages) {
+  PoolExtents x;
+  if (check_paged_decode(a, w, pages, x) || a->B == 0) return 0;
+  return (size_t)paged_workspace(paged_args(a, w, pages_of(pages, x)));
+}
+
+int dynconv_attn_paged_decode(const dynconv_attn *a, const dynconv_window *w, const dynconv_rotary *rot,
+                              const dynconv_view *q, const dynconv_view *k, const dynconv_view *v,
+                              const dynconv_pages *pages, const int32_t *lengths, const dynconv_view *o,
+                              void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  PoolExtents x;
+  int rc = check_paged_decode(a, w, pages, x);
+  if (rc || (rot && (rc = check_rotary(rot, a->head_dim)))) return rc;
+  if (rot && rot->inverse) return DYNCONV_E_SHAPE;
+  if (a->B == 0) return DYNCONV_OK;
+  const int64_t eb = a->dtype == DYNCONV_BF16 ? 2 : 4, H = a->n_heads, G = a->n_kv_heads, hd = a->head_dim;
+  if (!lengths) return DYNCONV_E_NULL;
+  Extent xq, xk, xv, xo;
+  if ((rc = extent(q, a->B, 1, H, hd, eb, true, xq)) || (rc = extent(k, a->B, 1, G, hd, eb, true, xk)) ||
+      (rc = extent(v, a->B, 1, G, hd, eb, true, xv)) || (rc = extent(o, a->B, 1, H, hd, eb, true, xo)))
+    return rc;
+  if (((uintptr_t)lengths & 3u) != 0 || ((uintptr_t)workspace & 15u) != 0) return DYNCONV_E_ALIGN;
+  PagedArgs r = paged_args(a, w, pages_of(pages, x));
+  const int64_t need = paged_workspace(r);
+  if (need > 0 && (!workspace || workspace_bytes < (size_t)need)) return DYNCONV_E_WORKSPACE;
+  const Extent xw = flat(need > 0 ? workspace : nullptr, need);
+  const Extent xn = flat(lengths, a->B * 4), xf = flat(rot ? rot->freqs : nullptr, rot ? rot->rot_dim / 2 * 8 : 0);
+  const Extent *ins[] = {&xq, &xk, &xv, &xn, &xf, &x.table}, *outs[] = {&xo, &x.k, &x.v, &xw};
+  for (int i = 0; i < 4; ++i) {
+    if (!outs[i]->p) continue;
+    if (i == 0 && !disjoint_rows(xo)) return DYNCONV_E_ALIAS;
+    for (const Extent *n : ins)
+      if (n->p && meet(*outs[i], *n)) return DYNCONV_E_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (meet(*outs[i], *outs[j])) return DYNCONV_E_ALIAS;
+  }
+  r.q = strided(xq);
+  r.k = strided(xk);
+  r.v = strided(xv);
+  r.o = strided(xo);
+  r.rot = rot ? rot->rot_dim : 0;
+  r.interleaved = rot && rot->interleaved != 0;
+  r.scale = scale_of(a);
+  r.factor = rot ? rot->factor : 1.f;
+  r.freqs = rot ? rot->freqs : nullptr;
+  r.lengths = lengths;
+  r.part = (float *)workspace;
+  const int64_t wide = std::min(16, r.H / r.G);
+  r.spans = (int2 *)((char *)workspace + 2 * r.blocks * wide * (hd + 2) * 4);
+  if ((rc = attn_paged(r, a->dtype, stream))) return rc;
   return attn_status();
 }
 

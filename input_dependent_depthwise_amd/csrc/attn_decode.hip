@@ -6,25 +6,11 @@
 // groups of 32 keys in turn, straight from memory to registers, each with its own running
 // maximum and sum, joined through LDS at the end.  Stretches of one sequence
 // are joined by a second kernel.
-//
-// No operand is moved between lanes on the way: in group coordinates key
-// 8u + 4t + r (u = 0..3 quarter of the wave, t = 0, 1, r = 0..3) is row 4u + r
-// of score tile t, so that a lane of quarter u holds the scores of keys 8u ..
-// 8u+7 of its column, which is the order of the second product's B operand; the
-// value rows 8u .. 8u+7 of lane c hold elements EV c .. EV c + EV - 1 of the
-// head, and the product's row c stands for element EV c + j in the j-th of EV
-// products.
-//
-// q (times scale and log2 e) and, for bf16 caches, the probabilities enter as
-// sums of two bf16 values, so their rounding does not show in o; the matrix
-// cores are idle enough for twice the products.  An infinity in the cache takes part in the
-// first of the two products alone (times a second part of 0 or of the other sign it would be
-// a NaN): a wave whose sums come out as NaN, as they do then, goes over its keys once more and takes
-// infinities and NaN out of the second products.
 #include <algorithm>
 #include <type_traits>
 
 #include "attn_decode.h"
+#include "attn_group.h"
 #include "kernels.h"
 #include "rope.h"
 
@@ -33,7 +19,6 @@ namespace dynconv {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kGroup = 32;                 // keys a wave takes at a time
 constexpr int kSorted = 256;               // sequences that are worth being put in order of length
 constexpr int kFloor = kWaves * kGroup;    // keys that are worth a block of their own
 
@@ -46,176 +31,48 @@ __device__ __forceinline__ int active_splits(int n, int n_split) {
   return max(1, (ng + per - 1) / per);
 }
 
-// o from the joined sums (t = 0: every score was -infinity, no key has a weight)
-__device__ __forceinline__ float quotient(float s, float t) { return t == 0.f ? 0.f : s / t; }
-
-template <typename T> struct Pair { uint4 hi, lo; };  // a B operand as hi + lo (fp32: hi alone)
-
-// bf16 rounding of 8 values and of what it left
-__device__ __forceinline__ Pair<bf16> split8(const float (&f)[8]) {
-  bf16x8 h, l;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    h[i] = (bf16)f[i];
-    l[i] = (bf16)(f[i] - (float)h[i]);
-  }
-  return {__builtin_bit_cast(uint4, h), __builtin_bit_cast(uint4, l)};
-}
-// the same of values that may be infinite: their first part alone
-__device__ __forceinline__ Pair<bf16> split8_any(const float (&f)[8]) {
-  bf16x8 h, l;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    h[i] = (bf16)f[i];
-    const float rest = f[i] - (float)h[i];
-    l[i] = (bf16)(__builtin_fabsf(rest) < INFINITY ? rest : 0.f);
-  }
-  return {__builtin_bit_cast(uint4, h), __builtin_bit_cast(uint4, l)};
-}
-
+// Keys row0 .. row0+31 of the cache, those below n.
 template <typename T, int DH>
-struct Group {
-  static constexpr int E = 16 / (int)sizeof(T), NS = DH / (4 * E), EV = DH / 16;
-  static constexpr int VW = EV * (int)sizeof(T) / 4;  // dwords of a value piece: 2, 4 or 8
-  uint4 k[2][NS];
-  uint32_t v[8][VW];
-
-  // keys row0 .. row0+31 of the cache, those below n
-  __device__ __forceinline__ void fetch(const char *kc, const char *vc, int64_t krow, int64_t vrow, int row0, int n,
-                                        int hd, int lane) {
-    const __amdgpu_buffer_rsrc_t rk = make_rsrc(kc + (int64_t)row0 * krow, kOutside);
-    const __amdgpu_buffer_rsrc_t rv = make_rsrc(vc + (int64_t)row0 * vrow, kOutside);
-    const int m = lane & 15, u = lane >> 4;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int row = 8 * (m >> 2) + 4 * t + (m & 3);
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int chunk = 4 * s + u;
-        const bool in = row0 + row < n && chunk * E < hd;
-        k[t][s] = buf_load16(rk, in ? (uint32_t)row * (uint32_t)krow + chunk * 16u : kOutside);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = 8 * u + i;
-      const uint32_t off = (uint32_t)row * (uint32_t)vrow + (uint32_t)(m * EV * (int)sizeof(T));
-      const bool there = row0 + row < n;
-      if constexpr (VW == 2) {
-        const uint2 x = buf_load8(rv, there && m * EV < hd ? off : kOutside);
-        v[i][0] = x.x;
-        v[i][1] = x.y;
-      } else {
-#pragma unroll
-        for (int w = 0; w < VW / 4; ++w) {
-          const uint4 x = buf_load16(rv, there && m * EV + w * E < hd ? off + 16u * w : kOutside);
-          v[i][4 * w] = x.x;
-          v[i][4 * w + 1] = x.y;
-          v[i][4 * w + 2] = x.z;
-          v[i][4 * w + 3] = x.w;
-        }
-      }
-    }
-  }
-};
-
-// Running softmax of a wave: its 16 columns' maximum, partial sum and values.
-template <typename T, int DH>
-struct State {
+__device__ __forceinline__ void fetch(Group<T, DH> &x, const char *kc, const char *vc, int64_t krow, int64_t vrow, int row0,
+                                      int n, int hd, int lane) {
   using G = Group<T, DH>;
-  float m, l;
-  f32x4 acc[G::EV];
-
-  __device__ __forceinline__ void clear() {
-    m = -INFINITY;
-    l = 0.f;
+  constexpr int E = G::E, NS = G::NS, EV = G::EV, VW = G::VW;
+  auto &k = x.k;
+  auto &v = x.v;
+  const __amdgpu_buffer_rsrc_t rk = make_rsrc(kc + (int64_t)row0 * krow, kOutside);
+  const __amdgpu_buffer_rsrc_t rv = make_rsrc(vc + (int64_t)row0 * vrow, kOutside);
+  const int m = lane & 15, u = lane >> 4;
 #pragma unroll
-    for (int j = 0; j < G::EV; ++j)
+  for (int t = 0; t < 2; ++t) {
+    const int row = 8 * (m >> 2) + 4 * t + (m & 3);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[j][r] = 0.f;
+    for (int s = 0; s < NS; ++s) {
+      const int chunk = 4 * s + u;
+      const bool in = row0 + row < n && chunk * E < hd;
+      k[t][s] = buf_load16(rk, in ? (uint32_t)row * (uint32_t)krow + chunk * 16u : kOutside);
+    }
   }
-  // Whether some lane's sum or value is a NaN (uniform).
-  __device__ __forceinline__ bool spoilt() const {
-    bool bad = l != l;
 #pragma unroll
-    for (int j = 0; j < G::EV; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) bad |= acc[j][r] != acc[j][r];
-    return __ballot(bad) != 0;
-  }
-
-  // GUARD: infinities and NaN of the cache enter the first products alone.
-  template <bool GUARD>
-  __device__ __forceinline__ void add(const G &x, const Pair<T> (&q)[G::NS], int first, int n, int lane) {
-    const int u = lane >> 4;
-    f32x4 s[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s[t][r] = 0.f;
-#pragma unroll
-      for (int i = 0; i < G::NS; ++i) {
-        if constexpr (sizeof(T) == 2) {
-          s[t] = mfma16(as_bf16x8(x.k[t][i]), as_bf16x8(q[i].hi), s[t]);
-          s[t] = mfma16(as_bf16x8(GUARD ? part_of<T, Part::KEEP>(x.k[t][i]) : x.k[t][i]), as_bf16x8(q[i].lo), s[t]);
-        } else {
-          const uint4 &a = x.k[t][i], &b = q[i].hi;
-          s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.x), __uint_as_float(b.x), s[t], 0, 0, 0);
-          s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.y), __uint_as_float(b.y), s[t], 0, 0, 0);
-          s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.z), __uint_as_float(b.z), s[t], 0, 0, 0);
-          s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.w), __uint_as_float(b.w), s[t], 0, 0, 0);
-        }
-      }
-    }
-    float mx = -INFINITY;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (first + 8 * u + 4 * t + r >= n) s[t][r] = -INFINITY;
-        mx = fmaxf(mx, s[t][r]);
-      }
-    mx = half_max(mx);
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    if (__ballot(mx > m) != 0) {
-      const float up = fmaxf(m, mx);
-      const float f = up == m ? 1.f : __builtin_amdgcn_exp2f(m - up);
-      m = up;
-      l *= f;
-#pragma unroll
-      for (int j = 0; j < G::EV; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[j][r] *= f;
-    }
-    const float m0 = m == -INFINITY ? 0.f : m;
-    float p[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(s[i >> 2][i & 3] - m0);
-      l += p[i];
-    }
-    if constexpr (sizeof(T) == 2) {
-      const Pair<bf16> pb = split8(p);
-#pragma unroll
-      for (int j = 0; j < G::EV; ++j) {
-        // element j of the 8 value rows: halves of dwords j/2 taken together
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = __builtin_amdgcn_perm(x.v[2 * i + 1][j / 2], x.v[2 * i][j / 2], (j & 1) ? 0x07060302u : 0x05040100u);
-        const uint4 a = make_uint4(w[0], w[1], w[2], w[3]);
-        acc[j] = mfma16(as_bf16x8(a), as_bf16x8(pb.hi), acc[j]);
-        acc[j] = mfma16(as_bf16x8(GUARD ? part_of<T, Part::KEEP>(a) : a), as_bf16x8(pb.lo), acc[j]);
-      }
+  for (int i = 0; i < 8; ++i) {
+    const int row = 8 * u + i;
+    const uint32_t off = (uint32_t)row * (uint32_t)vrow + (uint32_t)(m * EV * (int)sizeof(T));
+    const bool there = row0 + row < n;
+    if constexpr (VW == 2) {
+      const uint2 x = buf_load8(rv, there && m * EV < hd ? off : kOutside);
+      v[i][0] = x.x;
+      v[i][1] = x.y;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < G::EV; ++j)
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x.v[i][j]), p[i], acc[j], 0, 0, 0);
+      for (int w = 0; w < VW / 4; ++w) {
+        const uint4 x = buf_load16(rv, there && m * EV + w * E < hd ? off + 16u * w : kOutside);
+        v[i][4 * w] = x.x;
+        v[i][4 * w + 1] = x.y;
+        v[i][4 * w + 2] = x.z;
+        v[i][4 * w + 3] = x.w;
+      }
     }
   }
-};
+}
 
 template <typename T, int DH>
 __global__ __launch_bounds__(kWaves * 64, 1) void attn_decode_kernel(DecodeArgs a) {
@@ -261,7 +118,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void attn_decode_kernel(DecodeArgs 
   char *kc = a.kc.p + b * a.kc.batch + g * a.kc.head, *vc = a.vc.p + b * a.vc.batch + g * a.vc.head;
   GP x;
   const int row0 = first + wave * kGroup;
-  if (row0 < stop) x.fetch(kc, vc, a.kc.row, a.vc.row, row0, stop, a.hd, lane);
+  if (row0 < stop) fetch(x, kc, vc, a.kc.row, a.vc.row, row0, stop, a.hd, lane);
 
   // q and the new key, turned, in LDS; the new key and value into the cache
   for (int i = tid; i < 17 * LD; i += THREADS) (&qs[0][0])[i] = 0.f;
@@ -333,12 +190,12 @@ __global__ __launch_bounds__(kWaves * 64, 1) void attn_decode_kernel(DecodeArgs 
       const int next = row + kWaves * kGroup;
       if constexpr (AHEAD && !GUARD) {
         GP y;
-        if (next < stop) y.fetch(kc, vc, a.kc.row, a.vc.row, next, stop, a.hd, lane);
-        st.template add<GUARD>(x, q, row, stop, lane);
+        if (next < stop) fetch(y, kc, vc, a.kc.row, a.vc.row, next, stop, a.hd, lane);
+        st.template add<GUARD>(x, q, [=](int i) { return row + i < stop; }, lane);
         if (next < stop) x = y;
       } else {
-        st.template add<GUARD>(x, q, row, stop, lane);
-        if (next < stop) x.fetch(kc, vc, a.kc.row, a.vc.row, next, stop, a.hd, lane);
+        st.template add<GUARD>(x, q, [=](int i) { return row + i < stop; }, lane);
+        if (next < stop) fetch(x, kc, vc, a.kc.row, a.vc.row, next, stop, a.hd, lane);
       }
     }
     if (split == 0 && wave == kWaves - 1) {  // the new token: a group of one key (its wave has the fewest others)
@@ -368,13 +225,13 @@ __global__ __launch_bounds__(kWaves * 64, 1) void attn_decode_kernel(DecodeArgs 
           const int at = m16 * GP::EV * (int)sizeof(T) + 4 * w;
           y.v[i][w] = i == 0 && u4 == 0 && at < a.hd * (int)sizeof(T) ? *(const uint32_t *)(vs + at) : 0u;
         }
-      st.template add<GUARD>(y, q, 0, 1, lane);
+      st.template add<GUARD>(y, q, [](int i) { return i < 1; }, lane);
     }
   };
   pass(std::false_type());
   if constexpr (sizeof(T) == 2) {
     if (__builtin_expect(st.spoilt(), 0)) {
-      if (row0 < stop) x.fetch(kc, vc, a.kc.row, a.vc.row, row0, stop, a.hd, lane);
+      if (row0 < stop) fetch(x, kc, vc, a.kc.row, a.vc.row, row0, stop, a.hd, lane);
       pass(std::true_type());
     }
   }

@@ -51,3 +51,38 @@ def attention(q, k, v, window, sinks=0, scale=None, cu=None, d_o=None):
         if name in r:
             r[name] = math.sqrt(r[name])
     return r
+
+
+def paged_rows(table, n_pages, size, b, positions):
+    """(rows of the pool, which of them exist) of the given positions of sequence b."""
+    page = table[b].long()[positions // size]
+    ok = (page >= 0) & (page < n_pages)
+    return torch.where(ok, page, 0) * size + positions % size, ok
+
+
+def paged_decode(q, k_row, v, kp, vp, table, lengths, window=None, sinks=0, scale=None, freqs=None, interleaved=False,
+                 factor=1.0):
+    """o of one step over pools as they are before it, in fp64.  k_row [B, G, hd]: the new keys as they are stored."""
+    B, H, hd = q.shape
+    G, (n_pages, size) = k_row.shape[1], kp.shape[:2]
+    scale = 1 / math.sqrt(hd) if scale is None else scale
+    q = q.double()
+    if freqs is not None:
+        q = au.rotate(q[:, None].cpu(), freqs.cpu(), lengths.view(B, 1).cpu(), interleaved, factor)[:, 0].to(q.device)
+    o = torch.zeros_like(q)
+    for b, n in enumerate(lengths.tolist()):
+        if n < 0 or n >= table.shape[1] * size:
+            continue
+        j = torch.arange(n, device=q.device)
+        if window is not None:
+            j = j[(n - j < window) | (j < sinks)]
+        rows, ok = paged_rows(table, n_pages, size, b, j)
+        keys = torch.cat((kp.flatten(0, 1)[rows[ok]], k_row[b:b + 1].to(kp.dtype))).double()
+        values = torch.cat((vp.flatten(0, 1)[rows[ok]], v[b:b + 1])).double()
+        for h in range(H):
+            g = h // (H // G)
+            s = keys[:, g] @ q[b, h] * scale
+            if bool((s == -math.inf).all()):
+                continue
+            o[b, h] = au.seen_product(s.softmax(0)[None], values[:, g], (s == -math.inf)[None])[0]
+    return o
