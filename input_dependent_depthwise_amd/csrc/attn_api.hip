@@ -227,6 +227,7 @@ PagedArgs paged_args(const dynconv_attn *a, const dynconv_window *w, const Pages
   r.hd = a->head_dim;
   r.window = w && w->window < pages.capacity ? w->window : 0;
   r.sinks = r.window ? w->sinks : 0;
+  r.abreast = paged_abreast(r);
   r.blocks = paged_blocks(r);
   return r;
 }
@@ -598,7 +599,7 @@ int dynconv_attn_paged_decode(const dynconv_attn *a, const dynconv_window *w, co
   r.lengths = lengths;
   r.part = (float *)workspace;
   const int64_t wide = std::min(16, r.H / r.G);
-  r.spans = (int2 *)((char *)workspace + 2 * r.blocks * wide * (hd + 2) * 4);
+  r.spans = (int2 *)((char *)workspace + 2 * r.blocks * r.abreast * wide * (hd + 2) * 4);
   if ((rc = attn_paged(r, a->dtype, stream))) return rc;
   return attn_status();
 }

@@ -85,9 +85,9 @@ struct State {
   }
 
   // GUARD: infinities and NaN of the cache enter the first products alone.
-  // seen(i): whether the columns see key i of the group.
-  template <bool GUARD, typename SEEN>
-  __device__ __forceinline__ void add(const G &x, const Pair<T> (&q)[G::NS], SEEN seen, int lane) {
+  // q[i]: step i of the columns' operand; seen(i): whether they see key i of the group.
+  template <bool GUARD, typename Q, typename SEEN>
+  __device__ __forceinline__ void add(const G &x, const Q &q, SEEN seen, int lane) {
     const int u = lane >> 4;
     f32x4 s[2];
 #pragma unroll
@@ -96,11 +96,12 @@ struct State {
       for (int r = 0; r < 4; ++r) s[t][r] = 0.f;
 #pragma unroll
       for (int i = 0; i < G::NS; ++i) {
+        const Pair<T> c = q[i];
         if constexpr (sizeof(T) == 2) {
-          s[t] = mfma16(as_bf16x8(x.k[t][i]), as_bf16x8(q[i].hi), s[t]);
-          s[t] = mfma16(as_bf16x8(GUARD ? part_of<T, Part::KEEP>(x.k[t][i]) : x.k[t][i]), as_bf16x8(q[i].lo), s[t]);
+          s[t] = mfma16(as_bf16x8(x.k[t][i]), as_bf16x8(c.hi), s[t]);
+          s[t] = mfma16(as_bf16x8(GUARD ? part_of<T, Part::KEEP>(x.k[t][i]) : x.k[t][i]), as_bf16x8(c.lo), s[t]);
         } else {
-          const uint4 &a = x.k[t][i], &b = q[i].hi;
+          const uint4 &a = x.k[t][i], &b = c.hi;
           s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.x), __uint_as_float(b.x), s[t], 0, 0, 0);
           s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.y), __uint_as_float(b.y), s[t], 0, 0, 0);
           s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.z), __uint_as_float(b.z), s[t], 0, 0, 0);

@@ -29,10 +29,12 @@ struct PagedArgs {
   float scale, factor;
   const double *freqs;
   const int32_t *lengths;
-  int blocks;    // of the flattened launch, 0: a block for each sequence and key/value head
-  float *part;   // flattened: sums [2 blocks][cols][hd], then maximum and sum [2 blocks][cols][2]
-  int2 *spans;   // flattened: the first and the last block of each sequence and key/value head
+  int blocks;    // of the flat launch, 0: a block for each sequence and unit (key/value head and up to 16 query heads)
+  int abreast;   // flat: units of a sequence that a block takes side by side
+  float *part;   // flat: sums [2 blocks][abreast][columns][hd], then maximum and sum [2 blocks][abreast][columns][2]
+  int2 *spans;   // flat: the first and the last block of each sequence and unit
 };
+int paged_abreast(const PagedArgs &a);
 int paged_blocks(const PagedArgs &a);
 int64_t paged_workspace(const PagedArgs &a);
 int attn_paged(const PagedArgs &a, int dtype, hipStream_t st);
