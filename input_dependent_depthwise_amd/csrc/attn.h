@@ -37,6 +37,7 @@ struct AttnArgs {
   int n_seqs;
   int window, sinks;  // the windowed kernels: a query sees the last `window` tokens and the first `sinks` of its document
   float *far;         // their backward: dk / dv of sinks from the queries past their window, see far_rows
+  int far_chunk;      // queries that are summed together for it, whole blocks of 128
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -152,6 +153,8 @@ __device__ __forceinline__ uint4 score_frag(const f32x16 &p, int s) {
 // streamed row (of 32) that register i of a score block holds in half h
 __device__ __forceinline__ int score_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
 // Copies rows [row0, row0 + ROWS) of one head into a tile, through registers:
 // fetch() issues the loads, store() writes what came.  Rows at or past `limit`
 // and elements past head_dim come as zeros (of rows that overlap each other in
@@ -174,6 +177,21 @@ struct Stage {
     const uint32_t step = (uint32_t)R * (uint32_t)row_bytes;
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = buf_load16(rs, at + i * step);
+  }
+  // Whether the thread has an infinity or a NaN of them.
+  __device__ __forceinline__ bool not_finite() const {
+    u16x2 top16 = {0, 0};
+    uint32_t top32 = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 2) top16 = __builtin_elementwise_max(top16, __builtin_bit_cast(u16x2, w[k] & 0x7fff7fffu));
+        else top32 = max(top32, w[k] & 0x7fffffffu);
+      }
+    }
+    return sizeof(T) == 2 ? max(top16[0], top16[1]) >= 0x7f80u : top32 >= 0x7f800000u;
   }
   __device__ __forceinline__ void store(unsigned char *t, int tid) const {
     if (TL::NC < W && tid % W >= TL::NC) return;
@@ -253,7 +271,6 @@ __device__ __forceinline__ void arrived_acc(uint4 (&f)[N]) {
 
 // Whether rows r0 .. r0+31 of a tile hold an infinity or a NaN (uniform): the
 // largest bit pattern without its sign, two operations for a dword.
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 template <typename T, int DH>
 __device__ __forceinline__ bool not_finite(const unsigned char *t, int r0, int lane) {
   using TL = Tile<T, DH>;
@@ -395,28 +412,44 @@ __device__ __forceinline__ void write_row(char *row, const f32x16 (&acc)[DH / 32
 // with that the order of a block's key tiles: those of the sinks, if they lie before the window, then the window's.
 template <int BN, bool WIN>
 struct Window {
-  __device__ __forceinline__ void begin(const AttnArgs &, int, int, int, int &) {}
-  __device__ __forceinline__ bool sees(int) const { return true; }
+  int q, start;  // the lane's query and its document's start
+  __device__ __forceinline__ void begin(const AttnArgs &, int, int query, int from, int &) {
+    q = query;
+    start = from;
+  }
+  __device__ __forceinline__ bool sees(int key, bool) const { return key <= q && key >= start; }
+  __device__ __forceinline__ bool late(int, int) const { return true; }
   __device__ __forceinline__ bool part(int, int, int) const { return false; }
   __device__ __forceinline__ bool none(int, int, int) const { return false; }
   __device__ __forceinline__ int after(int kt) const { return kt + BN; }
   __device__ __forceinline__ int tile(int first, int i) const { return first + BN * i; }
+  __device__ __forceinline__ bool half(int) const { return false; }
 };
 template <int BN>
 struct Window<BN, true> {
   int size, sinks;     // the window's tokens, and the first ones of a document
   int hop_at, hop_to;  // the window's part of the tiles, see window_keys
-  int from, until;     // the lane's query sees keys >= from and keys < until
-  // q0: the block's first query; q, start: the lane's query and its document's start; first: the document's start of q0,
-  // the block's first key afterwards
-  __device__ __forceinline__ void begin(const AttnArgs &a, int q0, int q, int start, int &first) {
+  int far_end;         // the end of the sinks that lie before it
+  int q, start;        // the lane's query and its document's start
+  uint32_t reach, early;  // the keys it sees up to itself, and from the start on
+  // q0: the block's first query; first: the document's start of q0, the block's first key afterwards
+  __device__ __forceinline__ void begin(const AttnArgs &a, int q0, int query, int from, int &first) {
     size = a.window;
     sinks = a.sinks;
+    q = query;
+    start = from;
+    far_end = first + sinks;
     window_keys(size, sinks, BN, q0, first, hop_at, hop_to);
-    from = q - size + 1;
-    until = start + sinks;
+    const int before = greater(0, q - start + 1);
+    reach = lesser(size, before);
+    early = lesser(sinks, before);
   }
-  __device__ __forceinline__ bool sees(int key) const { return key >= from || key < until; }
+  // late: the tile has no sink of any of the wave's queries (one comparison for both ends of the window).
+  __device__ __forceinline__ bool sees(int key, bool late) const {
+    return (uint32_t)(q - key) < reach || (!late && (uint32_t)(key - start) < early);
+  }
+  // w_full: where the last of the wave's documents starts.
+  __device__ __forceinline__ bool late(int kt, int w_full) const { return kt >= w_full + sinks; }
   // Whether some of the 32 queries from qw on might not see some key of the tile; w_first: where lane 0's document starts
   // (the others' sinks end no earlier).
   __device__ __forceinline__ bool part(int kt, int qw, int w_first) const {
@@ -431,6 +464,8 @@ struct Window<BN, true> {
     const int kt = first + BN * i;
     return hop_at < 0 || kt < hop_at ? kt : hop_to + (kt - hop_at);
   }
+  // Whether the first 32 keys of the tile are all that it is there for: few sinks before the window.
+  __device__ __forceinline__ bool half(int kt) const { return kt < hop_at && kt + 32 >= far_end; }
 };
 
 // Waves of the forward and dq kernels on a SIMD: as many as the registers of a wave allow (3 and not 2
@@ -501,10 +536,15 @@ __device__ __forceinline__ void block_of(int n_heads_all, int &tile_rank, int &h
 
 // Rows of AttnArgs::far: sinks' sums of the queries past their window, [B][G][chunk][slot of its document][sink], one
 // slot a chunk without packing; none where no query lies past the window of the first 128 keys.
-__host__ __device__ __forceinline__ int far_slots(const AttnArgs &a) { return a.cu ? kFarSlots : 1; }
+__host__ __device__ __forceinline__ int far_slots(const AttnArgs &a) { return a.cu ? a.far_chunk / 128 : 1; }
 inline bool has_far(const AttnArgs &a) { return a.sinks > 0 && a.T > (int64_t)a.window + 127; }
+// Chunks of 128 queries, or more of them where that leaves two blocks for a CU.
+inline int far_chunk_of(const AttnArgs &a) {
+  const int64_t blocks = (int64_t)((a.T + 127) / 128) * a.G * a.B;
+  return 128 * (int)(blocks < 1024 ? 1 : blocks < 4096 ? blocks / 512 : 8);
+}
 inline int64_t far_rows(const AttnArgs &a) {
-  return has_far(a) ? (int64_t)a.B * a.G * ((a.T + kFarChunk - 1) / kFarChunk) * far_slots(a) * a.sinks : 0;
+  return has_far(a) ? (int64_t)a.B * a.G * ((a.T + a.far_chunk - 1) / a.far_chunk) * far_slots(a) * a.sinks : 0;
 }
 
 int attn_fwd(const AttnArgs &a, int dtype, hipStream_t st);

@@ -33,6 +33,7 @@ struct Dq {
   int qw, w_first, w_full;
   int q, start;  // the lane's query and its document's start
   Window<BN, WIN> win;
+  static constexpr bool STAGED = WIN;  // (as in the forward, here for the keys)
   float c;       // scale log2 e
   float lse2, delta;
   uint4 qf[TL::KS], df[TL::KS];
@@ -68,7 +69,7 @@ struct Dq {
         for (int i = 0; i < 16; ++i) {
           const int key = kt + 32 * n + score_row(i, h);
           const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -lse2)) * dp[i];
-          if (key <= q && key >= start && win.sees(key)) sum += x;
+          if (win.sees(key, false)) sum += x;
         }
       }
       __syncthreads();
@@ -96,14 +97,17 @@ struct Dq {
       p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -lse2)) * (dp[i] - delta);
     if (masked) {
       uint32_t seen = 0;
+      auto hide = [&](bool late) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int key = kt + score_row(i, h);
-        const bool see = key <= q && key >= start && win.sees(key);
-        if (!see) p[i] = 0.f;
-        seen |= (uint32_t)see << i;
-      }
-      sum_rows_masked<GUARD, T, DH>(kl, 32 * n, p, seen, acc, met, lane);
+        for (int i = 0; i < 16; ++i) {
+          const bool see = win.sees(kt + score_row(i, h), late);
+          if (!see) p[i] = 0.f;
+          seen |= (uint32_t)see << i;
+        }
+      };
+      if (win.late(kt, w_full)) hide(true);
+      else hide(false);
+      if constexpr (GUARD || !STAGED) sum_rows_masked<GUARD, T, DH>(kl, 32 * n, p, seen, acc, met, lane);
     }
     if (!GUARD || !masked) {
       sum_rows<T, DH>(kl, 32 * n, p, acc, lane);
@@ -128,7 +132,7 @@ struct Dq {
     for (int i = 0; i < 16; ++i) {
       const int key = kt + score_row(i, h);
       const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -lse2)) * dp[i];
-      if (key <= q && key >= start && win.sees(key)) sum += x;
+      if (win.sees(key, false)) sum += x;
     }
     wave_sync();
     return half_sum(sum);
@@ -145,6 +149,7 @@ struct Dq {
     if (kt <= last) {
       sk.fetch(kh, krow, kt, limit, hd, lane);
       sv.fetch(vh, vrow, kt, limit, hd, lane);
+      if constexpr (STAGED && !GUARD) met |= sk.not_finite();
       sk.store(mine[0], lane);
       sv.store(mine[1], lane);
     }
@@ -159,6 +164,7 @@ struct Dq {
       block<GUARD>(mine[0], mine[1], 0, kt, REST || kt + 31 > qw || kt < w_full || win.part(kt, qw, w_first), met, lane);
       wave_sync();
       if (more) {
+        if constexpr (STAGED && !GUARD) met |= sk.not_finite();
         sk.store(mine[0], lane);
         sv.store(mine[1], lane);
       }
@@ -177,6 +183,7 @@ struct Dq {
     if (first <= last) {
       sk.fetch(kh, krow, first, limit, hd, tid);
       sv.fetch(vh, vrow, first, limit, hd, tid);
+      if constexpr (STAGED && !GUARD) met |= sk.not_finite();
       sk.store(lds[0][0], tid);
       sv.store(lds[0][1], tid);
     }
@@ -192,16 +199,18 @@ struct Dq {
       if constexpr (GUARD || BN == 32) {
 #pragma unroll 1
         for (int n = 0; n < BN / 32; ++n)
-          if (work) block<GUARD>(kl, vl, n, kt + 32 * n, masked, met, lane);
+          if (work && !(n > 0 && win.half(kt))) block<GUARD>(kl, vl, n, kt + 32 * n, masked, met, lane);
         if (more) sv.fetch(vh, vrow, next, limit, hd, tid);
+        if (STAGED && !GUARD && more) met |= sk.not_finite();
         if (more) sk.store(lds[buf ^ 1][0], tid);
       } else {
         if (work) block<GUARD>(kl, vl, 0, kt, masked, met, lane);
         if (more) {
+          if constexpr (STAGED) met |= sk.not_finite();
           sk.store(lds[buf ^ 1][0], tid);
           sv.fetch(vh, vrow, next, limit, hd, tid);
         }
-        if (work) block<GUARD>(kl, vl, 1, kt + 32, masked, met, lane);
+        if (work && !win.half(kt)) block<GUARD>(kl, vl, 1, kt + 32, masked, met, lane);
       }
       if (more) sv.store(lds[buf ^ 1][1], tid);
       __syncthreads();
@@ -360,8 +369,8 @@ __global__ __launch_bounds__(256, sizeof(T) * DH > 256 ? 1 : 2) void attn_dq_few
 
 // The row of a sink in AttnArgs::far, [dk, dv][hd].
 __device__ __forceinline__ float *far_row(const AttnArgs &a, int b, int g, int chunk, int start, int sink, int which) {
-  const int64_t chunks = (a.T + kFarChunk - 1) / kFarChunk, n = far_slots(a);
-  const int64_t slot = (((int64_t)b * a.G + g) * chunks + chunk) * n + (a.cu ? far_slot(chunk, start) : 0);
+  const int64_t chunks = (a.T + a.far_chunk - 1) / a.far_chunk, n = far_slots(a);
+  const int64_t slot = (((int64_t)b * a.G + g) * chunks + chunk) * n + (a.cu ? far_slot(a.far_chunk, chunk, start) : 0);
   return a.far + ((slot * a.sinks + sink) * 2 + which) * a.hd;
 }
 constexpr int kFarKeys = 32;  // sinks whose sums are joined at a time
@@ -431,10 +440,11 @@ struct Dkv {
   // Which of the 32 queries from qt on see the lane's key; the others' scores to -infinity.
   __device__ __forceinline__ uint32_t hide(int qt, f32x16 &p, int lane) const {
     uint32_t seen = 0;
+    const uint32_t reach = greater(0, end - key);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int q = qt + score_row(i, lane >> 5);
-      const bool see = q >= key && q < end;
+      const bool see = WIN ? (uint32_t)(q - key) < reach : q >= key && q < end;
       if (!see) p[i] = -INFINITY;
       seen |= (uint32_t)see << i;
     }
@@ -497,7 +507,7 @@ struct Dkv {
         }
       }
     };
-    if (masked) {
+    if (!WIN && masked) {
 #pragma unroll
       for (int n = 0; n < NB; ++n) met |= not_finite<T, DH>(dl, 32 * n, lane) || not_finite<T, DH>(ql, 32 * n, lane);
     }
@@ -584,6 +594,7 @@ struct Dkv {
       }
     };
     auto store = [&](int to) {
+      if constexpr (WIN && !GUARD) met |= sq.not_finite() || sd.not_finite();  // (as in the forward)
       sq.store(lds.tile[to][0], tid);
       sd.store(lds.tile[to][1], tid);
       if (tid < 2 * BN) lds.stat[to][tid / BN][tid % BN] = st;
@@ -637,7 +648,7 @@ struct Dkv {
     doc_of(a.cu, a.n_seqs, a.T, limit, lesser(k0 + 127, limit - 1), start, unused);
     start = uniform(start);
     const int s0 = greater(k0, start), s1 = lesser(k0 + 128, start + a.sinks);  // the block's sinks
-    const int c0 = stop / kFarChunk, c1 = (doc_end - 1) / kFarChunk;
+    const int c0 = stop / a.far_chunk, c1 = (doc_end - 1) / a.far_chunk;
     const int quads = a.hd / 4;
     for (int s = s0; s < s1; s += kFarKeys) {
       const int n = lesser(kFarKeys, s1 - s);
@@ -763,13 +774,13 @@ __global__ __launch_bounds__(256, 1) void attn_far_kernel(AttnArgs a) {
     float sum[4][DH / 2][64];  // [wave][accumulator register][lane]
   } lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
-  const int chunks = (a.T + kFarChunk - 1) / kFarChunk;
+  const int chunks = (a.T + a.far_chunk - 1) / a.far_chunk;
   const int chunk = blockIdx.x % chunks, g = blockIdx.x / chunks % a.G, b = blockIdx.x / chunks / a.G;
   const int limit = uniform(tokens_in_docs(a.cu, a.n_seqs, a.T));
   const int per = a.H / a.G;
   const float c = a.scale * kLog2e;
   for (int m = 0, done = -1; m < far_slots(a); ++m) {
-    const int t = chunk * kFarChunk + (m ? 128 * m - 1 : 0);
+    const int t = chunk * a.far_chunk + (m ? 128 * m - 1 : 0);
     int start, end;
     doc_of(a.cu, a.n_seqs, a.T, limit, t, start, end);
     start = uniform(start);
@@ -779,8 +790,8 @@ __global__ __launch_bounds__(256, 1) void attn_far_kernel(AttnArgs a) {
     for (int s = start, n; s < lesser(start + a.sinks, end); s += n) {
       const int k0 = s / 128 * 128;  // the block of attn_dkv_kernel that the sink is in
       n = lesser(lesser(start + a.sinks, k0 + 128) - s, 32);
-      const int from = greater(chunk * kFarChunk, window_end(a.window, k0, 128, end));
-      const int to = lesser((chunk + 1) * kFarChunk, end);
+      const int from = greater(chunk * a.far_chunk, window_end(a.window, k0, 128, end));
+      const int to = lesser((chunk + 1) * a.far_chunk, end);
       if (from >= to) continue;
       const int key = s + (lane & 31);
       const bool there = (lane & 31) < n;
@@ -912,7 +923,7 @@ int launch_as(const AttnArgs &a, hipStream_t st) {
   else attn_dq_kernel<T, DH, BN, REST, WIN><<<dim3(n * a.H * a.B), dim3(256), 0, st>>>(a);
   if constexpr (WIN) {
     if (has_far(a))
-      attn_far_kernel<T, DH, REST><<<dim3((a.T + kFarChunk - 1) / kFarChunk * a.G * a.B), dim3(256), 0, st>>>(a);
+      attn_far_kernel<T, DH, REST><<<dim3((a.T + a.far_chunk - 1) / a.far_chunk * a.G * a.B), dim3(256), 0, st>>>(a);
   }
   attn_dkv_kernel<T, DH, BN, REST, WIN><<<dim3(n * a.G * a.n_split * a.B), dim3(256), 0, st>>>(a);
   if (a.n_split > 1) {

@@ -40,6 +40,9 @@ struct Fwd {
   int qw, w_first, w_full;
   int q, start;  // the lane's query and its document's start
   Window<BN, WIN> win;
+  // Through a window most tiles are masked for some wave: each thread looks for infinities and NaN in what it stages
+  // (all of the block's values then start over guarded), not each wave in each of its masked tiles.
+  static constexpr bool STAGED = WIN;
   float c;       // scale log2 e
   uint4 qf[TL::KS];
   f32x16 acc[TL::ND];
@@ -70,18 +73,21 @@ struct Fwd {
     }
     if constexpr (sizeof(T) == 2) read_ahead<BN / 32 * TL::KS, 1, 1, 4>();
     uint32_t seen[BN / 32];
-    if (masked) {
+    auto hide = [&](bool late) {
 #pragma unroll
       for (int n = 0; n < BN / 32; ++n) {
         seen[n] = 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int key = kt + 32 * n + score_row(i, h);
-          const bool see = key <= q && key >= start && win.sees(key);
+          const bool see = win.sees(kt + 32 * n + score_row(i, h), late);
           if (!see) p[n][i] = -INFINITY;
           seen[n] |= (uint32_t)see << i;
         }
       }
+    };
+    if (masked) {
+      if (win.late(kt, w_full)) hide(true);
+      else hide(false);
     }
     float mx = p[0][0];
 #pragma unroll
@@ -108,7 +114,7 @@ struct Fwd {
         p[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[n][i], c, -mc));
         l += p[n][i];
       }
-    if (masked) {
+    if (masked && (GUARD || !STAGED)) {
 #pragma unroll
       for (int n = 0; n < BN / 32; ++n)
         sum_rows_masked<GUARD, T, DH>(vl, 32 * n, p[n], seen[n], acc, met, lane);
@@ -139,6 +145,7 @@ struct Fwd {
     if (kt <= last) {
       sk.fetch(kh, krow, kt, limit, hd, lane);
       sv.fetch(vh, vrow, kt, limit, hd, lane);
+      if constexpr (STAGED && !GUARD) met |= sv.not_finite();
       sk.store(mine[0], lane);
       sv.store(mine[1], lane);
     }
@@ -153,6 +160,7 @@ struct Fwd {
       step<GUARD>(mine[0], mine[1], kt, met, lane);
       wave_sync();
       if (more) {
+        if constexpr (STAGED && !GUARD) met |= sv.not_finite();
         sk.store(mine[0], lane);
         sv.store(mine[1], lane);
       }
@@ -173,6 +181,7 @@ struct Fwd {
     if (first <= last) {
       sk.fetch(kh, krow, first, limit, hd, tid);
       sv.fetch(vh, vrow, first, limit, hd, tid);
+      if constexpr (STAGED && !GUARD) met |= sv.not_finite();
       sk.store(lds[0][0], tid);
       sv.store(lds[0][1], tid);
     }
@@ -189,6 +198,7 @@ struct Fwd {
         step<GUARD>(kl, vl, kt, met, lane);
       }
       if (more) {
+        if constexpr (STAGED && !GUARD) met |= sv.not_finite();
         sk.store(lds[buf ^ 1][0], tid);
         sv.store(lds[buf ^ 1][1], tid);
       }

@@ -574,7 +574,7 @@ int paged_abreast(const PagedArgs &a) {
 // Blocks of the flat launch; 0 where a block reads the most that a sequence can have in a few steps, or the batch is large.
 int paged_blocks(const PagedArgs &a) {
   const int64_t units = (int64_t)a.B * units_of(a), most = most_groups(a);
-  if (most <= 40 || a.B > kMostSeqs || units * most >= (int64_t)1 << 31) return 0;
+  if (most <= 96 || a.B > kMostSeqs || units * most >= (int64_t)1 << 31) return 0;
   return (int)std::min<int64_t>(kFlatWaves / paged_abreast(a), (units / paged_abreast(a) * most + kLeast - 1) / kLeast);
 }
 

@@ -79,12 +79,11 @@ __host__ __device__ __forceinline__ int window_end(int window, int k0, int rows,
   return w < end ? (int)w : end;
 }
 
-// Queries past window_end of their block of 128 keys are taken in chunks of kFarChunk, a slot for the sums of each document that
-// has any in the chunk.  Such a document holds the last token of a block of 128 keys: the chunk's
+// Queries past window_end of their block of 128 keys are taken in chunks of `size` (whole blocks), size / 128 slots for the
+// sums of the documents that have any in a chunk.  Such a document holds the last token of a block of 128 keys: the chunk's
 // first token belongs to the one of slot 0, and token 128 m - 1 of the chunk to the one of slot m if it starts inside.
-constexpr int kFarChunk = 512, kFarSlots = kFarChunk / 128;
-__host__ __device__ __forceinline__ int far_slot(int chunk, int start) {
-  const int c0 = chunk * kFarChunk;
+__host__ __device__ __forceinline__ int far_slot(int size, int chunk, int start) {
+  const int c0 = chunk * size;
   return start <= c0 ? 0 : (start - c0) / 128 + 1;
 }
 

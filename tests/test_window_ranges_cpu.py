@@ -29,7 +29,8 @@ static int fail(const char *what, const int32_t *cu, int n, int T, int W, int S,
   return 1;
 }
 
-static int check(const int32_t *cu, int n, int T, int W, int S, bool good) {
+static int check(const int32_t *cu, int n, int T, int W, int S, bool good, int kFarChunk) {
+  const int kFarSlots = kFarChunk / 128;
   const int limit = tokens_in_docs(cu, n, T);
   std::vector<int> start(T), end(T);
   for (int t = 0; t < T; ++t) doc_of(cu, n, T, limit, t, start[t], end[t]);
@@ -75,7 +76,7 @@ static int check(const int32_t *cu, int n, int T, int W, int S, bool good) {
       const int st = start[lesser(k0 + 127, limit - 1)];
       for (int s = greater(k0, st); s < lesser(k0 + 128, st + S); ++s)
         for (int c = stop / kFarChunk; c <= (doc_end - 1) / kFarChunk; ++c) {
-          const int slot = cu ? far_slot(c, st) : 0;
+          const int slot = cu ? far_slot(kFarChunk, c, st) : 0;
           if (slot < 0 || slot >= (cu ? kFarSlots : 1) || s - st < 0 || s - st >= S || c * kFarChunk >= T)
             return fail("read outside", cu, n, T, W, S, s);
           read.insert({c, slot, s});
@@ -89,7 +90,7 @@ static int check(const int32_t *cu, int n, int T, int W, int S, bool good) {
       doc_of(cu, n, T, limit, t, st, en);
       if (en == 0 || st == done) continue;
       done = st;
-      const int slot = cu ? far_slot(c, st) : 0;
+      const int slot = cu ? far_slot(kFarChunk, c, st) : 0;
       for (int s = st, k; s < lesser(st + S, en); s += k) {
         const int k0 = s / 128 * 128;
         k = lesser(lesser(st + S, k0 + 128) - s, 32);
@@ -126,7 +127,7 @@ int main() {
       for (int i = 1; i <= n; ++i)
         for (int j = i; j > 0 && cu[j] < cu[j - 1]; --j) { const int32_t x = cu[j]; cu[j] = cu[j - 1]; cu[j - 1] = x; }
     }
-    if (check(r % 5 ? cu : NULL, n, T, W, S, r % 5 ? good : true)) return 1;
+    if (check(r % 5 ? cu : NULL, n, T, W, S, r % 5 ? good : true, 128 << r % 4)) return 1;
   }
   printf("ok\n");
   return 0;
