@@ -410,6 +410,9 @@ __device__ __forceinline__ void write_row(char *row, const f32x16 (&acc)[DH / 32
 
 // Which keys the queries of the forward and dq kernels see of their document (WIN false: all earlier ones), and
 // with that the order of a block's key tiles: those of the sinks, if they lie before the window, then the window's.
+// In most masked tiles one end counts alone, the queries' own positions, the window's first token or the end of the sinks, and a
+// key costs one comparison with a constant.  The bounds and the masked scores pass through an empty asm: the compiler took the
+// comparisons out of their branches into every tile.
 template <int BN, bool WIN>
 struct Window {
   int q, start;  // the lane's query and its document's start
@@ -417,8 +420,11 @@ struct Window {
     q = query;
     start = from;
   }
-  __device__ __forceinline__ bool sees(int key, bool) const { return key <= q && key >= start; }
-  __device__ __forceinline__ bool late(int, int) const { return true; }
+  __device__ __forceinline__ bool sees(int key) const { return key <= q && key >= start; }
+  template <typename F>
+  __device__ __forceinline__ void masked(int kt, int, int, int, int lane, const F &hide) const {
+    hide([=](int i) { return sees(kt + 32 * (i >> 4) + score_row(i & 15, lane >> 5)); });
+  }
   __device__ __forceinline__ bool part(int, int, int) const { return false; }
   __device__ __forceinline__ bool none(int, int, int) const { return false; }
   __device__ __forceinline__ int after(int kt) const { return kt + BN; }
@@ -444,12 +450,34 @@ struct Window<BN, true> {
     reach = lesser(size, before);
     early = lesser(sinks, before);
   }
-  // late: the tile has no sink of any of the wave's queries (one comparison for both ends of the window).
-  __device__ __forceinline__ bool sees(int key, bool late) const {
-    return (uint32_t)(q - key) < reach || (!late && (uint32_t)(key - start) < early);
+  __device__ __forceinline__ bool sees(int key) const {
+    return (uint32_t)(q - key) < reach || (uint32_t)(key - start) < early;
   }
-  // w_full: where the last of the wave's documents starts.
-  __device__ __forceinline__ bool late(int kt, int w_full) const { return kt >= w_full + sinks; }
+  // hide(see) with see(i) for key i of the lane's scores (16 to a block of 32 keys) of the tile from kt on; qw, w_first, w_full:
+  // the wave's first query, where its first and its last document start.  (Queries of no document may
+  // see what they like here: nothing of theirs is written.)
+  template <typename F>
+  __device__ __forceinline__ void masked(int kt, int qw, int w_first, int w_full, int lane, const F &hide) const {
+    auto at = [](int i) { return 32 * (i >> 4) + score_row(i & 15, 0); };
+    const int own = kt + 4 * (lane >> 5);
+    if (kt > qw + 31 - size && kt >= w_full) {
+      int last = q - own;
+      asm volatile("" : "+v"(last));
+      hide([=](int i) { return at(i) <= last; });
+    } else if (kt + BN - 1 <= qw && kt >= w_full + sinks) {
+      int first = q - size + 1 - own;
+      asm volatile("" : "+v"(first));
+      hide([=](int i) { return at(i) >= first; });
+    } else if (kt + BN <= qw - size + 1 && w_first == w_full && kt >= w_first) {
+      int last = start + sinks - 1 - own;
+      asm volatile("" : "+v"(last));
+      hide([=](int i) { return at(i) <= last; });
+    } else {
+      int k0 = own;
+      asm volatile("" : "+v"(k0));
+      hide([=](int i) { return sees(k0 + at(i)); });
+    }
+  }
   // Whether some of the 32 queries from qw on might not see some key of the tile; w_first: where lane 0's document starts
   // (the others' sinks end no earlier).
   __device__ __forceinline__ bool part(int kt, int qw, int w_first) const {
@@ -538,10 +566,10 @@ __device__ __forceinline__ void block_of(int n_heads_all, int &tile_rank, int &h
 // slot a chunk without packing; none where no query lies past the window of the first 128 keys.
 __host__ __device__ __forceinline__ int far_slots(const AttnArgs &a) { return a.cu ? a.far_chunk / 128 : 1; }
 inline bool has_far(const AttnArgs &a) { return a.sinks > 0 && a.T > (int64_t)a.window + 127; }
-// Chunks of 128 queries, or more of them where that leaves two blocks for a CU.
-inline int far_chunk_of(const AttnArgs &a) {
-  const int64_t blocks = (int64_t)((a.T + 127) / 128) * a.G * a.B;
-  return 128 * (int)(blocks < 1024 ? 1 : blocks < 4096 ? blocks / 512 : 8);
+// Queries of a chunk: as few as leave one round of blocks for the chip (two on a CU with bf16 heads of up to 64), up to 1024.
+inline int far_chunk_of(const AttnArgs &a, bool two) {
+  const int64_t blocks = (int64_t)((a.T + 127) / 128) * a.G * a.B, at_once = two ? 512 : 256;
+  return 128 * (int)(blocks <= at_once ? 1 : blocks <= 8 * at_once ? (blocks + at_once - 1) / at_once : 8);
 }
 inline int64_t far_rows(const AttnArgs &a) {
   return has_far(a) ? (int64_t)a.B * a.G * ((a.T + a.far_chunk - 1) / a.far_chunk) * far_slots(a) * a.sinks : 0;

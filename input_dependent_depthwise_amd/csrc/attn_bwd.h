@@ -69,7 +69,7 @@ struct Dq {
         for (int i = 0; i < 16; ++i) {
           const int key = kt + 32 * n + score_row(i, h);
           const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -lse2)) * dp[i];
-          if (win.sees(key, false)) sum += x;
+          if (win.sees(key)) sum += x;
         }
       }
       __syncthreads();
@@ -89,7 +89,6 @@ struct Dq {
   template <bool GUARD>
   __device__ __forceinline__ void block(const unsigned char *kl, const unsigned char *vl, int n, int kt, bool masked,
                                         bool &met, int lane) {
-    const int h = lane >> 5;
     f32x16 p, dp;
     scores(kl, vl, n, p, dp, lane);
 #pragma unroll
@@ -97,16 +96,15 @@ struct Dq {
       p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -lse2)) * (dp[i] - delta);
     if (masked) {
       uint32_t seen = 0;
-      auto hide = [&](bool late) {
+      win.masked(kt, qw, w_first, w_full, lane, [&](auto see) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const bool see = win.sees(kt + score_row(i, h), late);
-          if (!see) p[i] = 0.f;
-          seen |= (uint32_t)see << i;
+          const bool s = see(i);
+          if (!s) p[i] = 0.f;
+          seen |= (uint32_t)s << i;
         }
-      };
-      if (win.late(kt, w_full)) hide(true);
-      else hide(false);
+        if constexpr (WIN) asm volatile("" : "+v"(p));
+      });
       if constexpr (GUARD || !STAGED) sum_rows_masked<GUARD, T, DH>(kl, 32 * n, p, seen, acc, met, lane);
     }
     if (!GUARD || !masked) {
@@ -132,7 +130,7 @@ struct Dq {
     for (int i = 0; i < 16; ++i) {
       const int key = kt + score_row(i, h);
       const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -lse2)) * dp[i];
-      if (win.sees(key, false)) sum += x;
+      if (win.sees(key)) sum += x;
     }
     wave_sync();
     return half_sum(sum);

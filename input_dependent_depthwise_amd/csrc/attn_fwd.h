@@ -61,7 +61,6 @@ struct Fwd {
   // The keys of one tile, from kt on.
   template <bool GUARD>
   __device__ __forceinline__ void step(const unsigned char *kl, const unsigned char *vl, int kt, bool &met, int lane) {
-    const int h = lane >> 5;
     const bool masked = (REST && BN == 32) || kt + BN - 1 > qw || kt < w_full || win.part(kt, qw, w_first);
     f32x16 p[BN / 32];
 #pragma unroll
@@ -73,22 +72,20 @@ struct Fwd {
     }
     if constexpr (sizeof(T) == 2) read_ahead<BN / 32 * TL::KS, 1, 1, 4>();
     uint32_t seen[BN / 32];
-    auto hide = [&](bool late) {
+    if (masked)
+      win.masked(kt, qw, w_first, w_full, lane, [&](auto see) {
 #pragma unroll
-      for (int n = 0; n < BN / 32; ++n) {
-        seen[n] = 0;
+        for (int n = 0; n < BN / 32; ++n) {
+          seen[n] = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool see = win.sees(kt + 32 * n + score_row(i, h), late);
-          if (!see) p[n][i] = -INFINITY;
-          seen[n] |= (uint32_t)see << i;
+          for (int i = 0; i < 16; ++i) {
+            const bool s = see(16 * n + i);
+            if (!s) p[n][i] = -INFINITY;
+            seen[n] |= (uint32_t)s << i;
+          }
+          if constexpr (WIN) asm volatile("" : "+v"(p[n]));
         }
-      }
-    };
-    if (masked) {
-      if (win.late(kt, w_full)) hide(true);
-      else hide(false);
-    }
+      });
     float mx = p[0][0];
 #pragma unroll
     for (int n = 0; n < BN / 32; ++n)

@@ -167,26 +167,50 @@ struct Wave {
   }
 
   // q and the new key, turned, in LDS, `sharers` waves taking part (this one is the i-th); the new key and value into their
-  // page.  A lane has one pair of the heads: its angle is formed once.
-  __device__ __forceinline__ void turn_pairs(const Part &p, int i, int sharers) {
+  // page.  A lane has one pair of the heads: its angle is formed once.  The first head's pair and the frequency are sent for ahead of
+  // the rows (loads come back in the order they were sent).
+  struct Pair0 {
+    double freq;
+    float u, w;
+  };
+  __device__ __forceinline__ const T *pair_source(const Part &p, int h) const {
+    return (const T *)(h == columns_of(p) ? a.k.p + p.b * a.k.batch + p.g * a.k.head
+                                          : a.q.p + p.b * a.q.batch + (first_head(p) + h) * a.q.head);
+  }
+  // Elements of pair m: halves or neighbours.
+  __device__ __forceinline__ int low(int m) const { return m < a.rot / 2 && !a.interleaved ? m : 2 * m; }
+  __device__ __forceinline__ int high(int m) const { return m < a.rot / 2 && !a.interleaved ? m + a.rot / 2 : 2 * m + 1; }
+  __device__ __forceinline__ Pair0 ask_pair(const Part &p, int i) const {
+    const int half = a.hd / 2, abreast = 64 / half, m = lane % half, h = i * abreast + lane / half;
+    Pair0 x = {0.0, 0.f, 0.f};
+    if (lane / half >= abreast || h > columns_of(p)) return x;
+    const T *src = pair_source(p, h);
+    if (m < a.rot / 2) x.freq = a.freqs[m];
+    x.u = to_f32(src[low(m)]);  // (rot is even: the rest starts at 2 (rot/2))
+    x.w = to_f32(src[high(m)]);
+    return x;
+  }
+  __device__ __forceinline__ void turn_pairs(const Part &p, Pair0 x, int i, int sharers) {
     const int half = a.hd / 2, abreast = 64 / half, m = lane % half, cols = columns_of(p), n = p.seen.n;
     const bool turned = m < a.rot / 2;
-    const int i0 = turned && !a.interleaved ? m : 2 * m;  // (rot is even: the rest starts at 2 (rot/2))
-    const int i1 = turned && !a.interleaved ? m + a.rot / 2 : 2 * m + 1;
+    const int i0 = low(m), i1 = high(m);
     float cs = 1.f, sn = 0.f;
     if (turned) {
-      turn(n, a.freqs[m], cs, sn);
+      turn(n, x.freq, cs, sn);
       cs *= a.factor;
       sn *= a.factor;
     }
     const float c = a.scale * kLog2e;
-    const char *q = a.q.p + p.b * a.q.batch + first_head(p) * a.q.head, *k = a.k.p + p.b * a.k.batch + p.g * a.k.head;
     const int first = i * abreast + lane / half;
     if (lane / half >= abreast) return;
 #pragma unroll 4
     for (int h = first; h <= cols; h += sharers * abreast) {
-      const T *src = (const T *)(h == cols ? k : q + h * a.q.head);
-      const float u = to_f32(src[i0]), w = to_f32(src[i1]);
+      float u = x.u, w = x.w;
+      if (h != first) {
+        const T *src = pair_source(p, h);
+        u = to_f32(src[i0]);
+        w = to_f32(src[i1]);
+      }
       float r0 = u, r1 = w;
       if (turned) turn_pair(u, w, cs, sn, r0, r1);
       float *to = qs + (h == cols ? wide : h) * LD;
@@ -328,8 +352,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_paged_kernel(PagedArgs a)
   }
   p.s1 = p.seen.groups;
   w.ask(p, wave, kWaves);
+  const typename W::Pair0 pair = w.ask_pair(p, wave);
   w.send(p, wave, kWaves);
-  w.turn_pairs(p, wave, kWaves);
+  w.turn_pairs(p, pair, wave, kWaves);
   __syncthreads();
   w.build(cols, wave, kWaves);
   __syncthreads();
@@ -429,7 +454,7 @@ __global__ __launch_bounds__(512, 2) void attn_paged_flat_kernel(PagedArgs a) {
   w.send(p, p.s0, 1);
   while (true) {
     const int cols = w.columns_of(p);
-    w.turn_pairs(p, 0, 1);
+    w.turn_pairs(p, w.ask_pair(p, 0), 0, 1);
     wave_sync();
     w.build(cols, 0, 1);
     wave_sync();

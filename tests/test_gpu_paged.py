@@ -105,6 +105,9 @@ CASES = [
     ([5000], 700, 8, 12, 12, 64),
     ([9000, 100], 300, 32, 4, 1, 128),
     ([2100, 2400, 3], 60, 40, 34, 2, 64),
+    ([4000, 2400, 0, 3999], 101, 40, 34, 2, 64),  # column blocks of 16 and 1 heads
+    ([3300, 70], 250, 16, 5, 5, 104),
+    ([3500, 3100, 900], 500, 8, 14, 14, 24),
 ]
 
 
@@ -126,6 +129,16 @@ def test_window(size, hd, window, sinks, dtype):
     lengths = [0, 1, 30, 64, 1500, 2000, -1, 65]
     _note(f"[paged] window {window} sinks {sinks} pages of {size} {hd} {dtype}")
     _step(lengths, 2040 // size, size, 4, 2, hd, dtype, window, sinks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("window,sinks", [(3400, 4), (3400, 128), (5000, 33)])
+@pytest.mark.parametrize("size,H,G,hd", [(16, 4, 2, 64), (7, 3, 3, 128), (64, 20, 1, 96)])
+def test_long_window(size, H, G, hd, window, sinks, dtype):
+    """Windows long enough that a sequence is shared among blocks."""
+    lengths = [0, 3399, 3401, 5950, -1, 6000, 5000, 40]
+    _note(f"[paged] window {window} sinks {sinks} pages of {size} {H} {G} {hd} {dtype}")
+    _step(lengths, 6100 // size, size, H, G, hd, dtype, window, sinks)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -280,7 +293,7 @@ def test_large_batches(B):
     r = torch.Generator().manual_seed(B)
     lengths = [int(x) for x in (torch.rand(B, generator=r) ** 6 * 3000).long()]
     lengths[5], lengths[B - 1], lengths[0] = -1, 2999, 0
-    _step(lengths, 94, 32, 4, 2, 64, "bf16")
+    _step(lengths, 120, 32, 4, 2, 64, "bf16")  # (lists long enough for the flat launch)
 
 
 def test_one_long_among_short():
@@ -438,7 +451,7 @@ def test_graph_replay():
     """Storing and steps in one graph whose lengths move on, with the eager calls between its replays; two graphs with one
     workspace, one after the other."""
     _note("[paged] graph")
-    B, H, G, hd, size, per_seq = 3, 8, 2, 64, 16, 150
+    B, H, G, hd, size, per_seq = 3, 8, 2, 64, 16, 250
     lengths = [1000, 37, -1]
     kp, vp, table = _cache(lengths, per_seq, size, G, hd, "bf16", 21)
     for b in range(2):  # pages for what follows
