@@ -455,16 +455,16 @@ def _pack_rotary(freqs: torch.Tensor, interleaved, inverse, factor, dev) -> byte
 
 def _pack_pages(k_pages, v_pages, table, lists, G, hd, dtype, dev) -> bytes:
     n, size = _dims(k_pages, "k_pages", 4)[:2]
-    pool = (n, size, G, hd)
-    for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        _pack_view(t, what, pool, dtype, dev)
-    entry = table.stride()
-    if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2 or table.shape[0] != lists or (
+    pool, sk, sv, entry = (n, size, G, hd), k_pages.stride(), v_pages.stride(), table.stride()
+    if (k_pages.shape != pool or v_pages.shape != pool or k_pages.dtype != dtype or v_pages.dtype != dtype or sk[-1] != 1
+            or sv[-1] != 1 or k_pages.get_device() != dev or v_pages.get_device() != dev):
+        _pack_view(k_pages, "k_pages", pool, dtype, dev)  # (says what is wrong, if anything is)
+        _pack_view(v_pages, "v_pages", pool, dtype, dev)
+    if table.dtype != torch.int32 or len(entry) != 2 or table.shape[0] != lists or not table.is_cuda or (
             entry[1] != 1 and table.shape[1] > 1):
         raise TypeError(f"page_table must be an int32 tensor [{lists}, pages] on the GPU with a contiguous last axis")
     if table.get_device() != dev:
         _other_device(table, "page_table", dev)
-    sk, sv = k_pages.stride(), v_pages.stride()
     return _PAGES(k_pages.data_ptr(), sk[0], sk[1], sk[2], v_pages.data_ptr(), sv[0], sv[1], sv[2], table.data_ptr(),
                   entry[0], n, table.shape[1], size, 0)
 

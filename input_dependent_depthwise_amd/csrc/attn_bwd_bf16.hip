@@ -23,7 +23,7 @@ int attn_bwd_splits(const AttnArgs &a, int dtype) {
     const double reach = (double)((std::min<int64_t>(a.T, (int64_t)a.window + 127) + 63) / 64) * (a.H / a.G);
     const double at_once = dtype == DYNCONV_BF16 && a.hd <= 64 ? 512 : 256;
     double least = 0;
-    for (int n = 1; n <= 8 && n <= reach; ++n) {
+    for (int n = 1; n <= 8 && n <= reach && n * blocks < (1 << 24); ++n) {
       const double us = std::ceil(blocks * n / at_once) * std::ceil(reach / n) * tile_us + (n > 1 ? n * split_us + join_us : 0.0);
       if (n == 1 || us < least) {
         least = us;

@@ -320,9 +320,12 @@ struct Wave {
     pass<false>(p, at, stride);
     if constexpr (sizeof(T) == 2) {
       if (__builtin_expect(st.spoilt(), 0)) {
+        const int next[2] = {ahead[0], ahead[1]};  // (of the part that was asked for after this one)
         ask(p, at, stride);
         send(p, at, stride);
         pass<true>(p, at, stride);
+        ahead[0] = next[0];
+        ahead[1] = next[1];
       }
     }
   }

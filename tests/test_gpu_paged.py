@@ -271,6 +271,23 @@ def test_seen_infinities(hd, n, dtype):
     assert bool((o[0, :, 0] == math.inf).all())
 
 
+@pytest.mark.parametrize("B", [40, 1000])
+def test_seen_infinities_among_many(B):
+    """A block takes several sequences one after another: one that starts over (an infinity among its values, behind its
+    first groups) leaves the next one as it is."""
+    _note(f"[paged] infinities among {B}")
+    lengths = [100, 40] * (B // 2)
+    kp, vp, table = _cache(lengths, 250, 16, 2, 64, "bf16", B)
+    for b in range(0, B, 2):
+        vp[int(table[b, 6]), 2, :, 5] = math.inf  # token 98
+    q, k, v = _new(B, 4, 2, 64, "bf16", B + 1)
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    ref = wu.paged_decode(q, k, v, kp, vp, table, n)
+    o = dc.dynconv_attn_paged_decode(q, k, v, kp, vp, table, n)
+    torch.cuda.synchronize()
+    assert au.rel(o, ref) <= TOL["bf16"]
+
+
 @pytest.mark.parametrize("n", [0, 40, 4000])
 def test_scores_that_are_all_minus_infinity(n):
     _note(f"[paged] all -infinity {n}")
