@@ -464,6 +464,58 @@ def test_prompt_then_steps_follow_the_whole_row(window, sinks, dtype):
         n += 1
 
 
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "qkv_attention.py")
+    spec = importlib.util.spec_from_file_location("qkv_attention", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    return ex
+
+
+def test_the_example_serves_from_pages():
+    """The example's ragged prompts and steps: within the roundings of the two ways (p of the whole-row call, the keys and
+    the outputs, 2^-8 each, of values that sum to the largest output), in fewer pages than the whole rows have."""
+    _note("[paged] example")
+    ex = _example()
+    off, size, pages = ex.serve()
+    assert math.isfinite(off) and off <= 4 * 2.0 ** -7 * size
+    assert pages < 3 * 12
+    assert all(math.isfinite(x) for x in ex.train(steps=2, window=40, sinks=2))
+
+
+def test_the_examples_gradients_through_a_window():
+    """The layer in fp32: the loss <o, w> along each parameter's gradient, against fourth-order differences.  A step of 1e-4
+    of the parameter's norm that way moves the loss by about 1e-4 sqrt(8192 parameters) = 1e-2 of its spread: the
+    differences' own error is (1e-2)^4, the loss' roundings (2^-20 of an output, at random) 1.5 * 2^-20 / 1e-2 = 1.4e-4."""
+    _note("[paged] example's gradients")
+    layer = _example().Layer(32, n_heads=4, n_kv_heads=2, head_dim=32, dtype=torch.float32, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    h = torch.randn(1, 130, 32, generator=g, device="cuda")
+    w = torch.randn(1, 130, 4, 32, generator=g, device="cuda").double()
+    cu = torch.tensor([0, 50, 130], dtype=torch.int32, device="cuda")
+
+    def loss():
+        return (layer.train(h, cu, 24, 2).double() * w).sum()
+
+    loss().backward()
+    for name in ("Wp", "W", "w0"):
+        p = getattr(layer, name)
+        start, grad = p.detach().clone(), p.grad
+        u = grad * (1e-4 * start.norm() / grad.norm())
+
+        def along(n):
+            with torch.no_grad():
+                p.copy_(start + n * u)
+                return loss().item()
+
+        diff = (8 * (along(1) - along(-1)) - (along(2) - along(-2))) / 12
+        along(0)
+        want = (grad.double() * u.double()).sum().item()
+        assert abs(diff - want) <= 1e-3 * want, (name, diff, want)
+
+
 def test_graph_replay():
     """Storing and steps in one graph whose lengths move on, with the eager calls between its replays; two graphs with one
     workspace, one after the other."""

@@ -106,11 +106,16 @@ def test_pointers_and_overlaps(L):
 
 def test_workspace_sizes(L):
     a = attn()
-    # a slot of 512 queries for each batch row and key/value head: dk and dv of each sink, fp32
-    assert need(L, a, Window(100, 4)) - need(L, a, Window(100, 0)) == 2 * 2 * 2 * 4 * 2 * 64 * 4
-    # packed: four documents' slots
+    # few tokens: a slot of 128 queries for each batch row and key/value head: dk and dv of each sink, fp32
+    assert need(L, a, Window(100, 4)) - need(L, a, Window(100, 0)) == 2 * 2 * 8 * 4 * 2 * 64 * 4
     p = attn(B=1, cu_seqlens=addr(20), n_seqs=3)
-    assert need(L, p, Window(100, 4)) - need(L, p, Window(100, 0)) == 2 * 2 * 4 * 4 * 2 * 64 * 4
+    assert need(L, p, Window(100, 4)) - need(L, p, Window(100, 0)) == 1 * 2 * 8 * 4 * 2 * 64 * 4
+    # 8 * 512 blocks of 128 queries: slots of 1024 queries, packed one for each document that can end in them (8)
+    a = attn(B=1, T=262144)
+    assert need(L, a, Window(100, 4)) - need(L, a, Window(100, 0)) == 2 * 256 * 4 * 2 * 64 * 4
+    p = attn(B=1, T=262144, cu_seqlens=addr(20), n_seqs=3)
+    assert need(L, p, Window(100, 4)) - need(L, p, Window(100, 0)) == 2 * 256 * 8 * 4 * 2 * 64 * 4
+    a = attn()
     # no query past the window of the first 128 keys; a window of the whole row is none
     assert need(L, a, Window(900, 4)) == need(L, a, Window(900, 0))
     assert need(L, a, Window(1000, 4)) == L.dynconv_attn_bwd_workspace_bytes(ref(a))
