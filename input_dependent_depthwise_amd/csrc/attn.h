@@ -566,10 +566,18 @@ __device__ __forceinline__ void block_of(int n_heads_all, int &tile_rank, int &h
 // slot a chunk without packing; none where no query lies past the window of the first 128 keys.
 __host__ __device__ __forceinline__ int far_slots(const AttnArgs &a) { return a.cu ? a.far_chunk / 128 : 1; }
 inline bool has_far(const AttnArgs &a) { return a.sinks > 0 && a.T > (int64_t)a.window + 127; }
-// Queries of a chunk: as few as leave one round of blocks for the chip (two on a CU with bf16 heads of up to 64), up to 1024.
-inline int far_chunk_of(const AttnArgs &a, bool two) {
-  const int64_t blocks = (int64_t)((a.T + 127) / 128) * a.G * a.B, at_once = two ? 512 : 256;
-  return 128 * (int)(blocks <= at_once ? 1 : blocks <= 8 * at_once ? (blocks + at_once - 1) / at_once : 8);
+// The sinks are summed 32 at a time, by blocks of their own where there are not many anyway.
+__host__ __device__ __forceinline__ int far_parts(const AttnArgs &a) { return (int64_t)a.B * a.G < 4096 ? (a.sinks + 31) / 32 : 1; }
+// Queries of a chunk, in 128s, up to 8: as few as leave one round of blocks for the chip (two on a CU with bf16 heads of up to
+// 64); more where a tile of sinks' dk/dv block, which adds its chunks one by one, would take longer for that (0.27 us for 32
+// sinks' chunk) than the chunk's tiles (1.5 us a 128 queries of a head in bf16, 8 in fp32).  One row of 3214 tokens, 2 heads of 64
+// and one key/value head, bf16, 128 sinks: far and dk/dv kernel 13 + 54 us with chunks of 128, 24 + 37 with the rule's.
+inline int far_chunk_of(const AttnArgs &a, bool is_bf16) {
+  const int64_t n = (a.T + 127) / 128, blocks = n * a.G * a.B * far_parts(a), at_once = is_bf16 && a.hd <= 64 ? 512 : 256;
+  int64_t k = blocks <= at_once ? 1 : blocks <= 8 * at_once ? (blocks + at_once - 1) / at_once : 8;
+  const int64_t added = n * a.sinks, tiles = (int64_t)(a.H / a.G) * (is_bf16 ? 180 : 950);
+  while (k < 8 && k * (k + 1) * tiles < added) ++k;
+  return 128 * (int)k;
 }
 inline int64_t far_rows(const AttnArgs &a) {
   return has_far(a) ? (int64_t)a.B * a.G * ((a.T + a.far_chunk - 1) / a.far_chunk) * far_slots(a) * a.sinks : 0;

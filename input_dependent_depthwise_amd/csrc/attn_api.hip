@@ -167,7 +167,7 @@ BwdPlan bwd_plan(const dynconv_attn *a, const dynconv_window *w) {
   AttnArgs r = attn_args(a);
   r.window = w ? w->window : 0;
   r.sinks = w ? w->sinks : 0;
-  r.far_chunk = far_chunk_of(r, a->dtype == DYNCONV_BF16 && a->head_dim <= 64);
+  r.far_chunk = far_chunk_of(r, a->dtype == DYNCONV_BF16);
   p.splits = attn_bwd_splits(r, a->dtype);
   p.delta = pad256(a->B * a->n_heads * a->T * 4);
   p.part = p.splits > 1 ? pad256((int64_t)2 * p.splits * a->B * a->n_kv_heads * a->T * a->head_dim * 4) : 0;
@@ -325,7 +325,7 @@ int backward(const dynconv_attn *a, const dynconv_window *w, const dynconv_view 
   r.n_split = p.splits;
   r.window = w ? w->window : 0;
   r.sinks = w ? w->sinks : 0;
-  r.far_chunk = far_chunk_of(r, a->dtype == DYNCONV_BF16 && a->head_dim <= 64);
+  r.far_chunk = far_chunk_of(r, a->dtype == DYNCONV_BF16);
   if ((rc = w ? attn_window_bwd(r, a->dtype, stream) : attn_bwd(r, a->dtype, stream))) return rc;
   return attn_status();
 }

@@ -638,6 +638,47 @@ struct Dkv {
     return met;
   }
 
+  // The chunks' sums of the sinks from s on, N values of a thread side by side, 8 or 16 loads on their way.
+  template <int N>
+  __device__ __forceinline__ void sum_far(FarLds<DH> &lds, int items, int c0, int c1, int g, int start, int s, int tid) {
+    const int quads = a.hd / 4;
+    for (int i0 = tid; i0 < items; i0 += 256 * N) {
+      float4 sum[N];
+      int kk[N], which[N], col[N];
+#pragma unroll
+      for (int m = 0; m < N; ++m) {
+        const int i = lesser(i0 + 256 * m, items - 1);  // (past the end: the last one once more)
+        kk[m] = i / (2 * quads);
+        which[m] = i / quads % 2;
+        col[m] = i % quads * 4;
+        sum[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      constexpr int U = N == 1 ? 8 : 4;
+      for (int c = c0; c < c1; c += U) {
+        float4 x[U][N];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int m = 0; m < N; ++m)
+            x[u][m] = *reinterpret_cast<const float4 *>(
+                far_row(a, b, g, lesser(c + u, c1 - 1), start, s + kk[m] - start, which[m]) + col[m]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (c + u >= c1) break;
+#pragma unroll
+          for (int m = 0; m < N; ++m) {
+            sum[m].x += x[u][m].x;
+            sum[m].y += x[u][m].y;
+            sum[m].z += x[u][m].z;
+            sum[m].w += x[u][m].w;
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < N; ++m) *reinterpret_cast<float4 *>(&lds.sum[kk[m]][which[m]][col[m]]) = sum[m];
+    }
+  }
+
   // WIN: what attn_far_kernel has summed for the block's sinks, chunk by chunk, from the first query past the window's on
   // to doc_end, the end of their document.
   __device__ __forceinline__ void add_far(FarLds<DH> &lds, int g, int doc_end, int tid, int lane) {
@@ -646,24 +687,17 @@ struct Dkv {
     doc_of(a.cu, a.n_seqs, a.T, limit, lesser(k0 + 127, limit - 1), start, unused);
     start = uniform(start);
     const int s0 = greater(k0, start), s1 = lesser(k0 + 128, start + a.sinks);  // the block's sinks
-    const int c0 = stop / a.far_chunk, c1 = (doc_end - 1) / a.far_chunk;
+    // (the splits of a block share the chunks)
+    const int first = stop / a.far_chunk, chunks = (doc_end - 1) / a.far_chunk + 1 - first;
+    const int c0 = first + chunks * split / a.n_split, c1 = first + chunks * (split + 1) / a.n_split;
+    if (c0 == c1) return;
     const int quads = a.hd / 4;
     for (int s = s0; s < s1; s += kFarKeys) {
       const int n = lesser(kFarKeys, s1 - s);
       __syncthreads();
-      for (int i = tid; i < n * 2 * quads; i += 256) {
-        const int kk = i / (2 * quads), which = i / quads % 2, col = i % quads * 4;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-          const float4 x = *reinterpret_cast<const float4 *>(far_row(a, b, g, c, start, s + kk - start, which) + col);
-          sum.x += x.x;
-          sum.y += x.y;
-          sum.z += x.z;
-          sum.w += x.w;
-        }
-        *reinterpret_cast<float4 *>(&lds.sum[kk][which][col]) = sum;
-      }
+      const int items = n * 2 * quads;
+      if (items <= 256) sum_far<1>(lds, items, c0, c1, g, start, s, tid);
+      else sum_far<4>(lds, items, c0, c1, g, start, s, tid);
       __syncthreads();
       if (key >= s && key < s + n) {
 #pragma unroll
@@ -739,7 +773,7 @@ __global__ __launch_bounds__(256, DH == 64 && sizeof(T) == 2 ? 2 : 1) void attn_
   const bool met = f.template pass<false>(lds, tid, lane);
   if (__builtin_expect(__syncthreads_or(met), 0)) f.template pass<true>(lds, tid, lane);
   if constexpr (WIN) {
-    if (f.stop < doc_end && split == 0 && a.sinks > 0) f.add_far(*(FarLds<DH> *)&lds, g, doc_end, tid, lane);
+    if (f.stop < doc_end && a.sinks > 0) f.add_far(*(FarLds<DH> *)&lds, g, doc_end, tid, lane);
   }
   if (key >= a.T) return;
   if (a.n_split == 1) {
@@ -773,7 +807,8 @@ __global__ __launch_bounds__(256, 1) void attn_far_kernel(AttnArgs a) {
   } lds;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = uniform(tid >> 6);
   const int chunks = (a.T + a.far_chunk - 1) / a.far_chunk;
-  const int chunk = blockIdx.x % chunks, g = blockIdx.x / chunks % a.G, b = blockIdx.x / chunks / a.G;
+  const int parts = far_parts(a), part = blockIdx.x / chunks % parts, bg = blockIdx.x / chunks / parts;
+  const int chunk = blockIdx.x % chunks, g = bg % a.G, b = bg / a.G;
   const int limit = uniform(tokens_in_docs(a.cu, a.n_seqs, a.T));
   const int per = a.H / a.G;
   const float c = a.scale * kLog2e;
@@ -785,12 +820,12 @@ __global__ __launch_bounds__(256, 1) void attn_far_kernel(AttnArgs a) {
     end = uniform(end);
     if (end == 0 || start == done) continue;
     done = start;
-    for (int s = start, n; s < lesser(start + a.sinks, end); s += n) {
+    for (int s = start, n, group = 0; s < lesser(start + a.sinks, end); s += n, ++group) {
       const int k0 = s / 128 * 128;  // the block of attn_dkv_kernel that the sink is in
       n = lesser(lesser(start + a.sinks, k0 + 128) - s, 32);
       const int from = greater(chunk * a.far_chunk, window_end(a.window, k0, 128, end));
       const int to = lesser((chunk + 1) * a.far_chunk, end);
-      if (from >= to) continue;
+      if (from >= to || group % parts != part) continue;
       const int key = s + (lane & 31);
       const bool there = (lane & 31) < n;
       const char *krow = a.k.p + b * a.k.batch + g * a.k.head + (int64_t)key * a.k.row;
@@ -921,7 +956,7 @@ int launch_as(const AttnArgs &a, hipStream_t st) {
   else attn_dq_kernel<T, DH, BN, REST, WIN><<<dim3(n * a.H * a.B), dim3(256), 0, st>>>(a);
   if constexpr (WIN) {
     if (has_far(a))
-      attn_far_kernel<T, DH, REST><<<dim3((a.T + a.far_chunk - 1) / a.far_chunk * a.G * a.B), dim3(256), 0, st>>>(a);
+      attn_far_kernel<T, DH, REST><<<dim3((a.T + a.far_chunk - 1) / a.far_chunk * far_parts(a) * a.G * a.B), dim3(256), 0, st>>>(a);
   }
   attn_dkv_kernel<T, DH, BN, REST, WIN><<<dim3(n * a.G * a.n_split * a.B), dim3(256), 0, st>>>(a);
   if (a.n_split > 1) {

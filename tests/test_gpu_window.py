@@ -142,6 +142,18 @@ def test_many_blocks_packed(heads, window, sinks, dtype):
         assert bool((got[n][:, 4100:] == 0).all()), n
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("cu", [None, [0, 1000, 2100], [0, 37, 130, 2000, 2090]])
+@pytest.mark.parametrize("heads", [(2, 1, 64), (8, 2, 128), (3, 3, 80)], ids=str)
+@pytest.mark.parametrize("window,sinks", [(3, 128), (200, 33), (90, 7)])
+def test_sinks_of_many_chunks(window, sinks, heads, cu, dtype):
+    """Few heads over a long row: sinks 32 at a time in blocks of their own, chunks of several blocks' queries, shared among
+    the splits of the sinks' tile, and added eight and four at a time."""
+    _note(f"[window] many chunks {heads} window {window} sinks {sinks} docs {cu} {dtype}")
+    q, k, v, d_o = _row(1, 2100, *heads, dtype, seed=window)
+    _compare(_run(q, k, v, d_o, window, sinks, cu=cu), wu.attention(q, k, v, window, sinks, cu=cu, d_o=d_o), dtype)
+
+
 @pytest.mark.parametrize("cu", [None, [0, 77, 200]])
 def test_a_window_of_the_whole_row_is_none(cu):
     """Bit for bit the call without a window, from T tokens on."""
