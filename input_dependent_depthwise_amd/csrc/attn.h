@@ -510,10 +510,14 @@ constexpr int waves() {
 // blocks, a quarter of the chain.  bf16, forward, without and with: 12 heads of 64, 1024 tokens
 // (96 blocks) 20 and 11 us; 8 of 128, 4096 (256) 87 and 74; 16 of 128, 4096 (512) 103 and 124;
 // 16 rows of 128 tokens, 12 of 64 (192): 8.1 and 9.9, a chain too short to be worth a join.
-constexpr int kFewBlocks = 256;
+// Through a short window chains are short, and the join costs more than it saves from fewer blocks on.  Forward and backward in us,
+// without and with, window of 128 and 4 sinks: heads of 128, bf16, 96 blocks 16 + 54 and 11 + 52, 192 17 + 61 and 19 + 67, 256
+// 17 + 63 and 20 + 73; fp32 96 53 + 156 and 36 + 135, 192 55 + 193 and 57 + 198; heads of 64, bf16, 192 12 + 42 and 12 + 44.
+// A window of 512: heads of 128, 192 blocks, bf16 25 + 82 and 26 + 89, fp32 111 + 374 and 101 + 360.
+constexpr int kFewBlocks = 256, kFewWindowBlocks = 160;
 inline bool few_blocks(const AttnArgs &a) {
   const int64_t blocks = (int64_t)((a.T + 127) / 128) * a.H * a.B;
-  return blocks <= kFewBlocks && blocks <= a.T / 2;
+  return blocks <= (a.window > 0 && a.window <= 512 ? kFewWindowBlocks : kFewBlocks) && blocks <= a.T / 2;
 }
 
 // Rows, or packed documents on average, short enough to take sum_rows_rest in their masked tiles, and
