@@ -724,6 +724,8 @@ class QKVAttnFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, row, n_heads, n_kv_heads, freqs, interleaved=False, factor=1.0, scale=None, cu_seqlens=None,
                 window=None, sinks=0):
+        if window is None and sinks != 0:
+            raise ValueError("sinks need a window")
         H, G = n_heads, n_kv_heads
         heads = row.view(row.shape[0], row.shape[1], H + 2 * G, row.shape[2] // (H + 2 * G))
         qk, v = heads[:, :, :H + G], heads[:, :, H + G:]

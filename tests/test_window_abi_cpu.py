@@ -131,3 +131,9 @@ def test_binding_refuses_before_the_call():
             dc.dynconv_attn_window_bwd(x, x, x, x, x, x, window, sinks=sinks)
     with pytest.raises(TypeError):
         dc.dynconv_attn_window_fwd(x, x, x, 4)  # not on the GPU
+
+
+def test_the_path_refuses_sinks_without_a_window():
+    row = torch.zeros(1, 4, 4 * 64)
+    with pytest.raises(ValueError, match="sinks need a window"):
+        dc.QKVAttnFn.apply(row, 2, 1, None, False, 1.0, None, None, None, 4)
