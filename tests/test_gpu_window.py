@@ -154,6 +154,36 @@ def test_sinks_of_many_chunks(window, sinks, heads, cu, dtype):
     _compare(_run(q, k, v, d_o, window, sinks, cu=cu), wu.attention(q, k, v, window, sinks, cu=cu, d_o=d_o), dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_past_4_gib(dtype):
+    """Rows a MiB apart: the last ones lie past 4 GiB from their tensor's start.  Bit for bit the call on dense tensors."""
+    _note(f"[window] rows a MiB apart {dtype}")
+    T, H, G, hd, window, sinks = 4500, 4, 2, 64, 70, 5
+    q, k, v, d_o = _row(1, T, H, G, hd, dtype, seed=8)
+    want = _run(q, k, v, d_o, window, sinks)
+    wide = torch.zeros(1, T, 2 ** 20 // q.element_size(), dtype=q.dtype, device="cuda")
+    at = 0
+
+    def place(x):
+        nonlocal at
+        n = x.shape[2] * hd
+        view = wide[:, :, at:at + n].view(1, T, x.shape[2], hd)
+        at += n
+        return view
+
+    ins = [place(x) for x in (q, k, v, d_o)]
+    for view, x in zip(ins, (q, k, v, d_o)):
+        view.copy_(x)
+    o = place(q)
+    o, lse = dc.dynconv_attn_window_fwd(*ins[:3], window, sinks=sinks, o=o, want_lse=True)
+    out = {"dq": place(q), "dk": place(k), "dv": place(v)}
+    dc.dynconv_attn_window_bwd(*ins[:3], o, lse, ins[3], window, sinks=sinks, out=out)
+    assert wide.stride(1) * wide.element_size() * (T - 1) > 2 ** 32
+    for n, x in {"o": o, "lse": lse, **out}.items():
+        assert torch.equal(x, want[n]), n
+    assert not wide[:, :, at:].any()
+
+
 @pytest.mark.parametrize("cu", [None, [0, 77, 200]])
 def test_a_window_of_the_whole_row_is_none(cu):
     """Bit for bit the call without a window, from T tokens on."""
