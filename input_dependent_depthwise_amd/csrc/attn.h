@@ -579,8 +579,9 @@ __host__ __device__ __forceinline__ int far_parts(const AttnArgs &a) { return (i
 // sinks' chunk) than the chunk's tiles (1.5 us a 128 queries of a head in bf16, 8 in fp32).  One row of 3214 tokens, 2 heads of 64
 // and one key/value head, bf16, 128 sinks: far and dk/dv kernel 13 + 54 us with chunks of 128, 24 + 37 with the rule's.
 inline int far_chunk_of(const AttnArgs &a, bool is_bf16) {
-  const int64_t n = (a.T + 127) / 128, blocks = n * a.G * a.B * far_parts(a), at_once = is_bf16 && a.hd <= 64 ? 512 : 256;
-  int64_t k = blocks <= at_once ? 1 : blocks <= 8 * at_once ? (blocks + at_once - 1) / at_once : 8;
+  const int64_t n = (a.T + 127) / 128, units = (int64_t)a.G * a.B * far_parts(a), at_once = is_bf16 && a.hd <= 64 ? 512 : 256;
+  int64_t k = 1;
+  while (k < 8 && (n + k - 1) / k * units > at_once) ++k;
   const int64_t added = n * a.sinks, tiles = (int64_t)(a.H / a.G) * (is_bf16 ? 180 : 950);
   while (k < 8 && k * (k + 1) * tiles < added) ++k;
   return 128 * (int)k;
