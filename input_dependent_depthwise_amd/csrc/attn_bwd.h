@@ -897,9 +897,9 @@ __global__ __launch_bounds__(256, 1) void attn_far_kernel(AttnArgs a) {
             mma_step<T>(TL::cols(ql, 0, x, d, lane), df, ak[d]);
           }
         }
-        if (REST) {
-          sum_rows_rest<false, T, DH>(dl, 0, p, av, lane);
-          sum_rows_rest<false, T, DH>(ql, 0, dp, ak, lane);
+        if (REST) {  // (every query sees every key here: an infinity has its part in the sums above)
+          sum_rows_rest<true, T, DH>(dl, 0, p, av, lane);
+          sum_rows_rest<true, T, DH>(ql, 0, dp, ak, lane);
         }
       }
       // the waves' sums, dk then dv

@@ -427,3 +427,43 @@ def test_autograd_of_the_path():
     back = au.rotate(torch.cat((ref["dq"], ref["dk"]), 2).cpu(), f.cpu(), pos.cpu(), inverse=True).cuda()
     want = torch.cat((back, ref["dv"]), 2).view(1, T, -1)
     assert au.rel(row.grad, want) <= au.TOL["fp32"]
+
+
+# As many documents as make a short row on average, one of them long.
+SHORT_ON_AVERAGE = [0, 600] + list(range(605, 701, 5))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("bad", BAD[:3], ids=str)
+@pytest.mark.parametrize("hd", [64, 80, 128])
+@pytest.mark.parametrize("window,sinks,cu", [(40, 3, None), (1, 63, None), (200, 4, None), (130, 128, None),
+                                             (200, 4, SHORT_ON_AVERAGE)], ids=["40-3", "1-63", "200-4", "130-128", "packed"])
+def test_far_gradients_that_are_not_finite(window, sinks, cu, hd, bad, dtype):
+    """Infinities and NaN in d_o of queries that see the sinks past the window: the sinks' dv holds them as the formula
+    does, with their sign (and their dk NaN: the query's d_o.v and d_o.o are the same infinity)."""
+    _note(f"[window] {bad} in d_o past the window {window} {sinks} hd={hd} {dtype}")
+    q, k, v, d_o = _row(1, 700, 4, 2, hd, dtype, seed=23)
+    v, d_o = v.clone(), d_o.clone()
+    v[..., 3], v[..., 5] = v[..., 3].abs() + 0.25, v[..., 5].abs() + 0.25
+    d_o[:, 520, 1, 3], d_o[:, 531, 2, 5] = bad, -bad
+    got, ref = _run(q, k, v, d_o, window, sinks, cu=cu), wu.attention(q, k, v, window, sinks, cu=cu, d_o=d_o)
+    if not math.isnan(bad):
+        assert bool((ref["dv"][:, :sinks, 0, 3] == bad).all()) and bool((ref["dv"][:, :sinks, 1, 5] == -bad).all())
+    errs = {n: au.rel(got[n], ref[n]) for n in ("o", "dq", "dk", "dv")}
+    assert all(e <= au.TOL[dtype] for e in errs.values()), errs
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("window,sinks", [(40, 3), (200, 4)])
+def test_gradients_of_a_sink_without_weight(window, sinks, dtype):
+    """A sink's key of -infinity where every query is positive: its weight is 0 everywhere, its own dk and dv are 0, and dq
+    holds the NaN of 0 x infinity in that element."""
+    _note(f"[window] -infinity in a sink's key {window} {sinks} {dtype}")
+    q, k, v, d_o = _row(1, 700, 4, 2, 64, dtype, seed=27)
+    q, k = q.clone(), k.clone()
+    q[..., 3] = q[..., 3].abs() + 0.25
+    k[:, 1, 0, 3] = -math.inf
+    got, ref = _run(q, k, v, d_o, window, sinks), wu.attention(q, k, v, window, sinks, d_o=d_o)
+    errs = {n: au.rel(got[n], ref[n]) for n in ("o", "dq", "dk", "dv")}
+    assert all(e <= au.TOL[dtype] for e in errs.values()), errs
+    assert bool((got["dk"][:, 1, 0] == 0).all()) and bool((got["dv"][:, 1, 0] == 0).all())
