@@ -476,7 +476,8 @@ __global__ __launch_bounds__(512, 2) void attn_paged_flat_kernel(PagedArgs a) {
     if (more) w.send(q, q.s0, 1);  // (while the sums are written)
     const float l = w.total();
     if (m16 < cols) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const bool none = l == 0.f;  // (as in quotient: whatever the values without a weight hold)
+      const float inv = none ? 0.f : 1.f / l;
       const int e = w.first_head(p) + m16;
       const int64_t row = ((int64_t)slot * a.abreast + wave) * wide + m16;
 #pragma unroll
@@ -486,7 +487,7 @@ __global__ __launch_bounds__(512, 2) void attn_paged_flat_kernel(PagedArgs a) {
           T *o = (T *)(a.o.p + p.b * a.o.batch + e * a.o.head) + d;
 #pragma unroll
           for (int j = 0; j < W::GP::EV; ++j)
-            if (d + j < a.hd) o[j] = from_f32<T>(w.st.acc[j][r] * inv);
+            if (d + j < a.hd) o[j] = from_f32<T>(none ? 0.f : w.st.acc[j][r] * inv);
         } else {
           float *o = a.part + row * a.hd + d;
 #pragma unroll

@@ -614,3 +614,33 @@ def test_pools_past_4_gib(dtype):
                 assert au.rel(o[b, h], p @ values[:, h]) <= TOL[dtype]
             page = int(table[b, m // size])
             assert torch.equal(kp[page, m % size], k[b]) and torch.equal(vp[page, m % size], v[b])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lengths,per_seq", [([40] * 3, 8), ([40] * 40, 250), ([40, 4000, 3, 0], 300)], ids=["whole", "flat", "joined"])
+def test_infinite_values_without_weight(lengths, per_seq, dtype):
+    """Scores that are all -infinity give zeros also where the values are infinite or NaN: taken whole, as one of several sequences
+    of a block, and joined from several blocks."""
+    _note(f"[paged] infinite values, scores all -infinity, {len(lengths)} {per_seq} {dtype}")
+    B, size = len(lengths), 16
+    kp, vp, table = _cache(lengths, per_seq, size, 2, 64, dtype, 51)
+    q, k, v = (t.clone() for t in _new(B, 4, 2, 64, dtype, 52))
+    q[:, :2, 3] = 1.0
+    k[:, 0, 3] = -math.inf
+    kp[:, :, 0, 3] = -math.inf
+    v[:, 0, 7] = math.inf
+    vp[:, 3, 0, 11], vp[:, 5, 0, 12] = -math.inf, math.nan
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    ref = wu.paged_decode(q, k, v, kp, vp, table, n)
+    o = dc.dynconv_attn_paged_decode(q, k, v, kp, vp, table, n)
+    torch.cuda.synchronize()
+    assert bool((o[:, :2] == 0).all()) and au.rel(o, ref) <= TOL[dtype]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("H,G", [(128, 8), (272, 16)], ids=["one column block", "two"])
+def test_eight_units_of_sixteen_heads_side_by_side(H, G, dtype):
+    """The flat launch at the most LDS it takes: eight waves of 16 query heads of 128 (two column blocks: four sets of them)."""
+    _note(f"[paged] {H} + {G} heads of 128 {dtype}")
+    _step([3300, 70, -1, 5000], 320, 16, H, G, 128, dtype)
+    _step([3300, 70, -1, 5000], 320, 16, H, G, 128, dtype, 4000, 5)
