@@ -189,7 +189,7 @@ int check_pages(const dynconv_attn *a, const dynconv_pages *p, int64_t lists, Po
   if (!p) return DYNCONV_E_NULL;
   if (p->n_pages <= 0 || p->pages_per_seq <= 0 || p->page_size <= 0) return DYNCONV_E_SHAPE;
   const int64_t lim = ((int64_t)1 << 31) - 4096;
-  if (p->n_pages > lim || p->pages_per_seq >= lim / p->page_size) return DYNCONV_E_LIMIT;
+  if (p->n_pages > lim || p->pages_per_seq > (lim - 1) / p->page_size) return DYNCONV_E_LIMIT;
   const int64_t eb = a->dtype == DYNCONV_BF16 ? 2 : 4, G = a->n_kv_heads, hd = a->head_dim;
   int rc;
   if ((rc = extent(&p->k, p->n_pages, p->page_size, G, hd, eb, true, x.k)) ||

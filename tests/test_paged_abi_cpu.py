@@ -222,3 +222,16 @@ def test_launches_go_to_the_tensors_gpu(monkeypatch):
         dc.dynconv_attn_paged_store(x, x, pool, pool, table)
         dc.dynconv_attn_window_fwd(x, x, x, 4, o=x)
     assert seen == [(i, 1000 + i) for i in (0, 0, 0, 1, 1, 1, 0, 0, 0)] and current == [0]
+
+
+@pytest.mark.parametrize("size,most", [((1 << 31) - 4097, 1), (1 << 30, 1), (300_000_000, 7), (1000, 2147479), (3, 715826517),
+                                       (1, (1 << 31) - 4097)])
+def test_positions_up_to_the_limit(L, size, most):
+    """page_size * pages_per_seq: the last product below 2^31 - 4096 is taken (what is refused then is the lengths' missing
+    address), one page more is not."""
+    assert size * most < (1 << 31) - 4096 <= size * (most + 1)
+    side_by_side = dict(k=View(addr(5), 0, 256, 64), v=View(addr(5) + 256, 0, 256, 64), table=addr(-200), n_pages=1, page_size=size)
+    assert step(L, attn(B=1), p=pages(pages_per_seq=most, table_row=0, **side_by_side), n=None) == NULL
+    assert step(L, attn(B=1), p=pages(pages_per_seq=most + 1, table_row=0, **side_by_side), n=None) == LIMIT
+    assert store(L, attn(B=1, T=30), p=pages(pages_per_seq=most, table_row=0, **side_by_side), k=View(None, 1, 1, 1)) == NULL
+    assert store(L, attn(B=1, T=30), p=pages(pages_per_seq=most + 1, table_row=0, **side_by_side), k=View(None, 1, 1, 1)) == LIMIT
