@@ -213,7 +213,6 @@ Pages pages_of(const dynconv_pages *p, const PoolExtents &x) {
   r.table_row = p->table_row;
   r.n_pages = (int)p->n_pages;
   r.size = p->page_size;
-  r.per_seq = (int)p->pages_per_seq;
   r.capacity = (int)(p->pages_per_seq * p->page_size);
   return r;
 }

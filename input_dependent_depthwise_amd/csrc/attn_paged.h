@@ -10,8 +10,8 @@ struct Pages {
   AttnView k, v;  // [n_pages, page_size, G, hd]: batch is the page's stride
   const int32_t *table;
   int64_t table_row;  // elements from one sequence's entries to the next one's
-  int n_pages, size, per_seq;
-  int capacity;  // per_seq * size
+  int n_pages, size;
+  int capacity;  // positions of a sequence's list
 };
 
 // Where row `slot` of a page starts in its pool.
