@@ -66,6 +66,7 @@ struct Fwd {
   // The keys of one tile, from kt on.
   template <bool GUARD>
   __device__ __forceinline__ void step(const unsigned char *kl, const unsigned char *vl, int kt, bool &met, int lane) {
+    const int h = lane >> 5;
     const bool masked = (REST && BN == 32) || kt + BN - 1 > qw || kt < w_full || win.part(kt, qw, w_first);
     f32x16 p[BN / 32];
 #pragma unroll
@@ -77,20 +78,34 @@ struct Fwd {
     }
     if constexpr (sizeof(T) == 2) read_ahead<BN / 32 * TL::KS, 1, 1, 4>();
     uint32_t seen[BN / 32];
-    if (masked)
-      win.masked(kt, qw, w_first, w_full, lane, [&](auto see) {
+    if (masked) {
+      if constexpr (WIN) {
+        win.masked(kt, qw, w_first, w_full, lane, [&](auto see) {
+#pragma unroll
+          for (int n = 0; n < BN / 32; ++n) {
+            seen[n] = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const bool s = see(16 * n + i);
+              if (!s) p[n][i] = -INFINITY;
+              seen[n] |= (uint32_t)s << i;
+            }
+            asm volatile("" : "+v"(p[n]));
+          }
+        });
+      } else {  // (passed as a function, these comparisons of all keys were held at once: 43 to 56 scalars spilled)
 #pragma unroll
         for (int n = 0; n < BN / 32; ++n) {
           seen[n] = 0;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const bool s = see(16 * n + i);
+            const bool s = win.sees(kt + 32 * n + score_row(i, h));
             if (!s) p[n][i] = -INFINITY;
             seen[n] |= (uint32_t)s << i;
           }
-          if constexpr (WIN) asm volatile("" : "+v"(p[n]));
         }
-      });
+      }
+    }
     float mx = p[0][0];
 #pragma unroll
     for (int n = 0; n < BN / 32; ++n)
