@@ -553,7 +553,7 @@ def dynconv_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, o=None, lse=None, 
     1 / sqrt(head_dim).  cu_seqlens: packed documents (B must be 1)."""
     if stream is not None:
         return _on(stream, dynconv_attn_fwd, q, k, v, scale=scale, cu_seqlens=cu_seqlens, o=o, lse=lse, want_lse=want_lse)
-    return _forward("dynconv_attn_fwd", (), q, k, v, scale, cu_seqlens, o, lse, want_lse)
+    return _forward("dynconv_attn_fwd", lib().dynconv_attn_fwd, (), q, k, v, scale, cu_seqlens, o, lse, want_lse)
 
 
 def dynconv_attn_window_fwd(q, k, v, window, *, sinks=0, scale=None, cu_seqlens=None, o=None, lse=None, want_lse=False,
@@ -564,12 +564,16 @@ def dynconv_attn_window_fwd(q, k, v, window, *, sinks=0, scale=None, cu_seqlens=
     if stream is not None:
         return _on(stream, dynconv_attn_window_fwd, q, k, v, window, sinks=sinks, scale=scale, cu_seqlens=cu_seqlens, o=o,
                    lse=lse, want_lse=want_lse)
-    return _forward("dynconv_attn_window_fwd", (_pack_window(window, sinks),), q, k, v, scale, cu_seqlens, o, lse, want_lse)
+    return _forward("dynconv_attn_window_fwd", lib().dynconv_attn_window_fwd, (_pack_window(window, sinks),), q, k, v, scale,
+                    cu_seqlens, o, lse, want_lse)
 
 
-def _forward(name, window, q, k, v, scale, cu_seqlens, o, lse, want_lse):
-    B, T, H, hd = shape = _dims(q, "q", 4)
-    G, dt, dev = _dims(k, "k", 4)[2], q.dtype, q.get_device()
+def _forward(name, call, window, q, k, v, scale, cu_seqlens, o, lse, want_lse):
+    shape, kv = q.shape, k.shape
+    if len(shape) != 4 or len(kv) != 4:
+        _dims(q, "q", 4), _dims(k, "k", 4)
+    B, T, H, hd = shape
+    G, dt, dev = kv[2], q.dtype, q.get_device()
     kv = (B, T, G, hd)
     vq, a = _pack_view(q, "q", shape, dt, dev), _pack_attn(B, T, H, G, hd, dt, dev, scale, cu_seqlens)
     o, vo = _out(o, q, "o", shape, dev)
@@ -580,8 +584,7 @@ def _forward(name, window, q, k, v, scale, cu_seqlens, o, lse, want_lse):
         pl = lse.data_ptr()
     else:
         pl = None
-    _launch(dev, name, getattr(lib(), name), a, *window, vq, _pack_view(k, "k", kv, dt, dev),
-            _pack_view(v, "v", kv, dt, dev), vo, pl)
+    _launch(dev, name, call, a, *window, vq, _pack_view(k, "k", kv, dt, dev), _pack_view(v, "v", kv, dt, dev), vo, pl)
     return (o, lse) if want_lse else o
 
 
@@ -592,7 +595,9 @@ def dynconv_attn_bwd(q, k, v, o, lse, d_o, *, scale=None, cu_seqlens=None, out=N
     if stream is not None:
         return _on(stream, dynconv_attn_bwd, q, k, v, o, lse, d_o, scale=scale, cu_seqlens=cu_seqlens, out=out,
                    workspace=workspace)
-    return _backward("dynconv_attn_bwd", (), q, k, v, o, lse, d_o, scale, cu_seqlens, out, workspace)
+    L = lib()
+    return _backward("dynconv_attn_bwd", L.dynconv_attn_bwd, L.dynconv_attn_bwd_workspace_bytes, (), q, k, v, o, lse, d_o, scale,
+                     cu_seqlens, out, workspace)
 
 
 def dynconv_attn_window_bwd(q, k, v, o, lse, d_o, window, *, sinks=0, scale=None, cu_seqlens=None, out=None,
@@ -602,13 +607,17 @@ def dynconv_attn_window_bwd(q, k, v, o, lse, d_o, window, *, sinks=0, scale=None
     if stream is not None:
         return _on(stream, dynconv_attn_window_bwd, q, k, v, o, lse, d_o, window, sinks=sinks, scale=scale,
                    cu_seqlens=cu_seqlens, out=out, workspace=workspace)
-    return _backward("dynconv_attn_window_bwd", (_pack_window(window, sinks),), q, k, v, o, lse, d_o, scale, cu_seqlens,
-                     out, workspace)
+    L = lib()
+    return _backward("dynconv_attn_window_bwd", L.dynconv_attn_window_bwd, L.dynconv_attn_window_bwd_workspace_bytes,
+                     (_pack_window(window, sinks),), q, k, v, o, lse, d_o, scale, cu_seqlens, out, workspace)
 
 
-def _backward(name, window, q, k, v, o, lse, d_o, scale, cu_seqlens, out, workspace):
-    B, T, H, hd = shape = _dims(q, "q", 4)
-    G, dt, dev = _dims(k, "k", 4)[2], q.dtype, q.get_device()
+def _backward(name, call, workspace_bytes, window, q, k, v, o, lse, d_o, scale, cu_seqlens, out, workspace):
+    shape, kv = q.shape, k.shape
+    if len(shape) != 4 or len(kv) != 4:
+        _dims(q, "q", 4), _dims(k, "k", 4)
+    B, T, H, hd = shape
+    G, dt, dev = kv[2], q.dtype, q.get_device()
     kv = (B, T, G, hd)
     ins = (_pack_view(q, "q", shape, dt, dev), _pack_view(k, "k", kv, dt, dev), _pack_view(v, "v", kv, dt, dev),
            _pack_view(o, "o", shape, dt, dev), _lse(lse, (B, H, T), dev), _pack_view(d_o, "d_o", shape, dt, dev))
@@ -617,9 +626,8 @@ def _backward(name, window, q, k, v, o, lse, d_o, scale, cu_seqlens, out, worksp
     dq, vdq = _out(out.get("dq"), q, "dq", shape, dev)
     dk, vdk = _out(out.get("dk"), k, "dk", kv, dev)
     dv, vdv = _out(out.get("dv"), v, "dv", kv, dev)
-    L = lib()
-    ws = _workspace(getattr(L, name + "_workspace_bytes")(a, *window), q.device, workspace)
-    _launch(dev, name, getattr(L, name), a, *window, *ins, vdq, vdk, vdv, ws.data_ptr(), ws.nbytes)
+    ws = _workspace(workspace_bytes(a, *window), q.device, workspace)
+    _launch(dev, name, call, a, *window, *ins, vdq, vdk, vdv, ws.data_ptr(), ws.nbytes)
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
