@@ -395,9 +395,9 @@ def _pack_view(t: torch.Tensor, what: str, shape, dtype, dev: int) -> bytes:
     """The View of a [B, T, heads, head_dim] (or [B, heads, head_dim]) tensor of the given shape and dtype on GPU dev."""
     if t.shape != shape:
         raise ValueError(f"{what}: expected the shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype or not t.is_cuda:
-        raise TypeError(f"{what}: expected a {dtype} tensor on the GPU, got {t.dtype} on {t.device}")
-    if t.get_device() != dev:
+    if t.dtype != dtype or t.get_device() != dev or dev < 0:
+        if t.dtype != dtype or not t.is_cuda:
+            raise TypeError(f"{what}: expected a {dtype} tensor on the GPU, got {t.dtype} on {t.device}")
         _other_device(t, what, dev)
     s = t.stride()
     if s[-1] != 1 and shape[-1] > 1 and t.numel():
