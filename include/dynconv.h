@@ -517,7 +517,9 @@ typedef struct {
  *   of sequence i (counts must be NULL).
  * The table has B (n_seqs) lists.  A sequence with starts < 0 is idle; tokens
  * at positions past the list, or of no document, are not stored.  Keys are rounded
- * to the I/O dtype once.  No workspace.
+ * to the I/O dtype once.  No workspace.  Pages are read by the one-token step
+ * alone: a prompt whose tokens are to attend to each other goes through
+ * dynconv_attn_fwd as a whole row, whatever starts says here.
  */
 DYNCONV_API int dynconv_attn_paged_store(const dynconv_attn *a, const dynconv_rotary *r, const dynconv_view *k,
                                          const dynconv_view *v, const dynconv_pages *pages, const int32_t *starts,
@@ -532,7 +534,8 @@ DYNCONV_API int dynconv_attn_paged_store(const dynconv_attn *a, const dynconv_ro
  * >= pages_per_seq * page_size is idle: its o is zero, and nothing is stored.
  * workspace: 16-byte aligned, at least
  * dynconv_attn_paged_decode_workspace_bytes(a, w, pages); it may be 0 bytes.
- * The size depends on the sizes in a, w and pages alone.
+ * The size depends on the sizes in a, w and pages alone; it is 0 for what the
+ * call refuses, pools and a table without an address among it.
  */
 DYNCONV_API size_t dynconv_attn_paged_decode_workspace_bytes(const dynconv_attn *a, const dynconv_window *w,
                                                              const dynconv_pages *pages);
