@@ -72,8 +72,8 @@ def cpu_model() -> str:
 
 
 # Sources each roofline kernel is built from (its own file, the headers it
-# includes, the public header): a traffic record counts only while these are
-# unchanged.
+# includes, the convolution's part of the public header): a traffic record
+# counts only while these are unchanged.
 KERNEL_SOURCES = {
     ("bwd_conv", "headwise"): ["conv_bwd_headwise.hip"],
     ("bwd_conv", "lowrank"): ["conv_bwd_lowrank.hip", "mfma.h"],
@@ -81,6 +81,8 @@ KERNEL_SOURCES = {
     ("fwd_conv", "lowrank"): ["conv_fwd_lowrank.hip", "mfma.h"],
 }
 COMMON_SOURCES = ["bufio.h", "common.h", "kernels.h", "../../include/dynconv.h"]
+# the public header's section of other calls, which none of these kernels is built from
+AFTER_CONVOLUTION = b"---- What follows the convolution"
 # the symbol of each roofline kernel in a rocprofv3 trace (substring)
 KERNEL_SYMBOLS = {("bwd_conv", "headwise"): "k_bwd_hw", ("bwd_conv", "lowrank"): "k_bwd_lr",
                   ("fwd_conv", "headwise"): "k_fwd_h", ("fwd_conv", "lowrank"): "k_fwd_lowrank"}
@@ -91,7 +93,10 @@ def kernel_source_sha(kernel: str, kind: str) -> str:
     csrc = os.path.join(ROOT, "input_dependent_depthwise_amd", "csrc")
     for f in KERNEL_SOURCES[(kernel, kind)] + COMMON_SOURCES:
         with open(os.path.join(csrc, f), "rb") as fh:
-            h.update(os.path.basename(f).encode() + fh.read())
+            text = fh.read()
+        if os.path.basename(f) == "dynconv.h":
+            text = text[:text.index(AFTER_CONVOLUTION)]
+        h.update(os.path.basename(f).encode() + text)
     return h.hexdigest()[:16]
 
 
