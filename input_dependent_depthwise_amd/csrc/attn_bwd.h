@@ -19,6 +19,8 @@
 // in dk/dv); 12 heads of 64, 8 rows of 2048, window of 256: 45, 62, 15, 76.
 #pragma once
 
+#include <type_traits>
+
 #include "attn.h"
 #include "kernels.h"
 
@@ -843,10 +845,6 @@ __global__ __launch_bounds__(256, 1) void attn_far_kernel(AttnArgs a) {
         vf[i] = owned_chunk<T, DH>(vrow, there, 2 * i + h, a.hd);
       }
       f32x16 ak[TL::ND], av[TL::ND];
-#pragma unroll
-      for (int d = 0; d < TL::ND; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) ak[d][i] = av[d][i] = 0.f;
       const int tiles = (to - from + 31) / 32, work = tiles * per;
       unsigned char(&ql)[TL::bytes(32)] = lds.in.tile[wave][0], (&dl)[TL::bytes(32)] = lds.in.tile[wave][1];
       float(&stat)[2][32] = lds.in.stat[wave];
@@ -865,42 +863,58 @@ __global__ __launch_bounds__(256, 1) void attn_far_kernel(AttnArgs a) {
           st = q < to ? a.delta[at] : 0.f;
         }
       };
-      if (wave < work) fetch(wave);
-      for (int it = wave; it < work; it += 4) {
-        wave_sync();
-        sq.store(ql, lane);
-        sd.store(dl, lane);
-        stat[h][lane & 31] = st;
-        wave_sync();
-        if (it + 4 < work) fetch(it + 4);
-        f32x16 p, dp;
+      // The wave's tiles; whether it met an infinity or a NaN (REST; GUARD: never).  Every query sees every key here, so
+      // these have their part in the first products: the others leave them out.
+      auto pass = [&](auto guard) {
+        constexpr bool GUARD = decltype(guard)::value;
+        bool met = false;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = dp[i] = 0.f;
+        for (int d = 0; d < TL::ND; ++d)
 #pragma unroll
-        for (int i = 0; i < TL::KS; ++i) mma_step<T>(TL::rows(ql, 0, i, lane), kf[i], p);
+          for (int i = 0; i < 16; ++i) ak[d][i] = av[d][i] = 0.f;
+        if (wave < work) fetch(wave);
+        for (int it = wave; it < work; it += 4) {
+          if constexpr (REST && !GUARD) met |= sq.not_finite() || sd.not_finite();
+          wave_sync();
+          sq.store(ql, lane);
+          sd.store(dl, lane);
+          stat[h][lane & 31] = st;
+          wave_sync();
+          if (it + 4 < work) fetch(it + 4);
+          f32x16 p, dp;
 #pragma unroll
-        for (int i = 0; i < TL::KS; ++i) mma_step<T>(TL::rows(dl, 0, i, lane), vf[i], dp);
-        const int left = to - (from + it % tiles * 32);  // queries of the tile
+          for (int i = 0; i < 16; ++i) p[i] = dp[i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = score_row(i, h);
-          p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -stat[0][r]));
-          dp[i] = p[i] * (dp[i] - stat[1][r]);
-          if (r >= left) p[i] = dp[i] = 0.f;  // (a zero row times an infinite key is a NaN)
-        }
+          for (int i = 0; i < TL::KS; ++i) mma_step<T>(TL::rows(ql, 0, i, lane), kf[i], p);
 #pragma unroll
-        for (int x = 0; x < TL::PS; ++x) {
-          const uint4 pf = score_frag<T>(p, x), df = score_frag<T>(dp, x);
+          for (int i = 0; i < TL::KS; ++i) mma_step<T>(TL::rows(dl, 0, i, lane), vf[i], dp);
+          const int left = to - (from + it % tiles * 32);  // queries of the tile
 #pragma unroll
-          for (int d = 0; d < TL::ND; ++d) {
-            mma_step<T>(TL::cols(dl, 0, x, d, lane), pf, av[d]);
-            mma_step<T>(TL::cols(ql, 0, x, d, lane), df, ak[d]);
+          for (int i = 0; i < 16; ++i) {
+            const int r = score_row(i, h);
+            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], c, -stat[0][r]));
+            dp[i] = p[i] * (dp[i] - stat[1][r]);
+            if (r >= left) p[i] = dp[i] = 0.f;  // (a zero row times an infinite key is a NaN)
+          }
+#pragma unroll
+          for (int x = 0; x < TL::PS; ++x) {
+            const uint4 pf = score_frag<T>(p, x), df = score_frag<T>(dp, x);
+#pragma unroll
+            for (int d = 0; d < TL::ND; ++d) {
+              mma_step<T>(TL::cols(dl, 0, x, d, lane), pf, av[d]);
+              mma_step<T>(TL::cols(ql, 0, x, d, lane), df, ak[d]);
+            }
+          }
+          if (REST) {
+            sum_rows_rest<GUARD, T, DH>(dl, 0, p, av, lane);
+            sum_rows_rest<GUARD, T, DH>(ql, 0, dp, ak, lane);
           }
         }
-        if (REST) {  // (every query sees every key here: an infinity has its part in the sums above)
-          sum_rows_rest<true, T, DH>(dl, 0, p, av, lane);
-          sum_rows_rest<true, T, DH>(ql, 0, dp, ak, lane);
-        }
+        return met;
+      };
+      const bool met = pass(std::false_type());
+      if constexpr (REST) {
+        if (__builtin_expect(__ballot(met) != 0, 0)) pass(std::true_type());
       }
       // the waves' sums, dk then dv
 #pragma unroll
