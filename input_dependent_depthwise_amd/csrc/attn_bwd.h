@@ -15,8 +15,8 @@
 //
 // Through a window a key is seen by as many queries; sinks are seen by all that follow, which would be one block's
 // work: attn_far_kernel sums them for the queries past the window and dk/dv adds its sums.  16 + 4 heads of 128, 8192 tokens in
-// 2 documents, window of 1024, 4 sinks, bf16: forward 96, dq 130, sinks 19, dk/dv 240 us (matrix cores 36 % busy in dq, 29 %
-// in dk/dv); 12 heads of 64, 8 rows of 2048, window of 256: 45, 62, 15, 76.
+// 2 documents, window of 1024, 4 sinks, bf16: forward 96 to 102 with the card, dq 130 to 138, sinks 19, dk/dv 240 to 247 us (matrix
+// cores 36 % busy in dq, 29 % in dk/dv); 12 heads of 64, 8 rows of 2048, window of 256: 45, 62, 14, 76.
 #pragma once
 
 #include <type_traits>

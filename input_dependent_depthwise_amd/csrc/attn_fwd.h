@@ -27,10 +27,11 @@ namespace {
 // busy with the exponentials and what surrounds them.  Tiles of 64 keys: 32 took 96 us where 64
 // take 82 (heads of 64, two waves), 128 took 123 (registers).
 //
-// Through a window: 16 + 4 heads of 128, 16384 tokens in 3 documents, window of 1024, 4 sinks, bf16: 186 us, 0.67 PFLOP/s of
-// the pairs that are seen (matrix cores 34 % busy, vector units 42 %: of 19 tiles of 64 keys that a block of 128 queries
-// reads three hold the window's ends and one the sinks, and four waves wait for each); 12 heads of 64, 8 rows of 2048,
-// window of 256: 41 to 47 us with the card, 2.2 to 2.5 TB/s (20 and 52 %: half of a block's 7 tiles are masked).
+// Through a window: 16 + 4 heads of 128, 16384 tokens in 3 documents, window of 1024, 4 sinks, bf16: 186 to 205 us with the
+// card, 0.61 to 0.67 PFLOP/s of the pairs that are seen (matrix cores 34 % busy, vector units 42 %: of 19 tiles of 64 keys
+// that a block of 128 queries reads three hold the window's ends and one the sinks, and four waves wait for each); 12 heads
+// of 64, 8 rows of 2048, window of 256: 41 to 47 us with the card, 2.2 to 2.5 TB/s (20 and 52 %: half of a block's 7 tiles
+// are masked).
 constexpr float kSlack = 8.f;
 
 template <typename T, int DH, int BN, bool REST, bool WIN>

@@ -31,8 +31,9 @@ namespace dynconv {
 namespace {
 
 constexpr int kMostSeqs = 1024;   // whose lengths a block of the flat launch adds up
-// of the flat launch, four a CU (the 64 sequences of up to 8191 tokens: 119 us; 2048: 121, 4096: 135; blocks of one wave
-// instead of side by side: 140)
+// of the flat launch: with 4 key/value heads side by side a block of four for each CU (64 sequences of up to 8191 tokens, 16 + 4 heads
+// of 128: 119 us; 2048: 121, 4096: 135; blocks of one wave instead of side by side: 140).  With 6 heads and more blocks are of
+// 6 to 8 waves and fewer than the CUs: 24 + 6 heads 220 us, 32 + 8 328, 16 + 16 604, 4.2, 3.8 and 4.1 TB/s against 5.3.
 constexpr int kFlatWaves = 1024;
 
 __device__ const uint4 kZeroRow[32] = {};  // stands for a row that is not there
@@ -608,7 +609,8 @@ int paged_abreast(const PagedArgs &a) {
 
 // Blocks of the flat launch; 0 where a block reads the most that a sequence can have in a few steps, or the batch is large.
 // A unit whole and flat, us, bf16: 64 windows of 1024, 16 + 4 heads of 128, 29 and 45; one sequence of 1024, 12 heads of 64, 12
-// and 21; 64 sequences of up to 4095, 16 + 4 heads of 128, 84 and 74.
+// and 21; 64 sequences of up to 4095, 16 + 4 heads of 128, 84 and 74.  What a sequence can have is what the rule knows: one of 1024
+// tokens in a table of 8192 takes the flat launch too, 20 us.
 int paged_blocks(const PagedArgs &a) {
   const int64_t units = (int64_t)a.B * units_of(a), most = most_groups(a);
   if (most <= 96 || a.B > kMostSeqs || units * most >= (int64_t)1 << 31) return 0;
